@@ -10,4 +10,6 @@ from .api import (combine, combine_add_rmsnorm, combine_from_peers, dispatch,  #
                   dispatch_quant, dispatch_to_peers, group_quant, peer_table, plan, plan_noalloc,
                   plan_outputs,
                   plan_dedup, plan_weight_rows, plan_workspace, quant_msg_bytes, remap_prune, ungroup)
+from .experts import (Q4Weights, expert_matvec_q4, moe_layer, moe_layer_workspace,  # noqa: F401
+                      q4_pack, q4_quantize, route, route_grad)
 from ._binding import MepError, lib  # noqa: F401

@@ -16,6 +16,8 @@ LIB_PATH = os.path.join(_HERE, "libmep.so")
 MEP_OK, MEP_ERR_NULLPTR, MEP_ERR_PARAM, MEP_ERR_SHAPE, MEP_ERR_HIP = range(5)
 MEP_SCALE_F32, MEP_SCALE_BF16, MEP_SCALE_F16 = 0, 1, 2
 MEP_PLAN_NOALLOC_SCRATCH_BYTES = 4 << 20  # include/mep.h
+MEP_SCORE_SOFTMAX, MEP_SCORE_SIGMOID = 0, 1
+MEP_WEIGHT_BF16, MEP_WEIGHT_INT4, MEP_WEIGHT_FP4 = 0, 1, 2
 
 _lib = None
 
@@ -24,6 +26,12 @@ class MepError(RuntimeError):
     def __init__(self, name, code, msg):
         super().__init__(f"{name} returned {code}: {msg}")
         self.code = code
+
+
+class Weights(ctypes.Structure):
+    """mep_weights (include/mep.h)."""
+    _fields_ = [(n, ctypes.c_int) for n in ("kind", "E", "N", "K", "group", "scale_dtype")] + [
+        (n, ctypes.c_void_p) for n in ("data", "scales", "zeros")]
 
 
 def lib():
@@ -74,6 +82,25 @@ def lib():
     L.mep_plan_dedup_workspace_size.restype = Z
     L.mep_plan_dedup.argtypes = [I, I, I, I, P, P, P, Z, P, P, P, P, P]
     L.mep_plan_dedup.restype = I
+    F, W = ctypes.c_float, ctypes.POINTER(Weights)
+    L.mep_route.argtypes = [I, I, I, P, I, P, I, I, I, I, F, P, P, P]
+    L.mep_route.restype = I
+    L.mep_route_grad.argtypes = [I, I, I, P, I, P, P, I, I, F, P, P]
+    L.mep_route_grad.restype = I
+    L.mep_packed_code_bytes.argtypes = [I, I, I]
+    L.mep_packed_code_bytes.restype = Z
+    L.mep_packed_scale_count.argtypes = [I, I, I, I]
+    L.mep_packed_scale_count.restype = Z
+    L.mep_pack_weights.argtypes = [I, I, I, I, I] + [P] * 7
+    L.mep_pack_weights.restype = I
+    L.mep_quant_weights.argtypes = [I, I, I, I, I, I, P, P, P, P]
+    L.mep_quant_weights.restype = I
+    L.mep_expert_matvec.argtypes = [I, I, I, P, I, P, P, W, P, P, P]
+    L.mep_expert_matvec.restype = I
+    L.mep_moe_layer_workspace_size.argtypes = [I, I, I]
+    L.mep_moe_layer_workspace_size.restype = Z
+    L.mep_moe_layer.argtypes = [I, I, I, I, I, P, P, P, P, W, W, P, Z, P, P, P]
+    L.mep_moe_layer.restype = I
     _lib = L
     return L
 
@@ -182,3 +209,49 @@ def mep_plan_dedup(R, S, K, my_rank, route_dest, route_slot, workspace, workspac
     return lib().mep_plan_dedup(R, S, K, my_rank, route_dest, route_slot, workspace,
                                 workspace_bytes, dpack_pos, dsend_count, drecv_pos, drecv_count,
                                 stream)
+
+
+def mep_route(T, E, K, logits, logit_dtype, bias, scoring, n_group, topk_group, renormalize,
+              scale, topk_ids, scores, stream) -> int:
+    return lib().mep_route(T, E, K, logits, logit_dtype, bias, scoring, n_group, topk_group,
+                           renormalize, scale, topk_ids, scores, stream)
+
+
+def mep_route_grad(T, E, K, logits, logit_dtype, topk_ids, dscores, scoring, renormalize, scale,
+                   dlogits, stream) -> int:
+    return lib().mep_route_grad(T, E, K, logits, logit_dtype, topk_ids, dscores, scoring,
+                                renormalize, scale, dlogits, stream)
+
+
+def mep_packed_code_bytes(E, N, K) -> int:
+    return lib().mep_packed_code_bytes(E, N, K)
+
+
+def mep_packed_scale_count(E, N, K, group) -> int:
+    return lib().mep_packed_scale_count(E, N, K, group)
+
+
+def mep_pack_weights(E, N, K, kind, group, codes, scales, zeros, packed_codes, packed_scales,
+                     packed_zeros, stream) -> int:
+    return lib().mep_pack_weights(E, N, K, kind, group, codes, scales, zeros, packed_codes,
+                                  packed_scales, packed_zeros, stream)
+
+
+def mep_quant_weights(E, N, K, kind, group, scale_dtype, w, codes, scales, stream) -> int:
+    return lib().mep_quant_weights(E, N, K, kind, group, scale_dtype, w, codes, scales, stream)
+
+
+def mep_expert_matvec(T, R, first, x, x_per_route, ids, mask, w, out_bf16, out_f32,
+                      stream) -> int:
+    return lib().mep_expert_matvec(T, R, first, x, x_per_route, ids, mask, w, out_bf16, out_f32,
+                                   stream)
+
+
+def mep_moe_layer_workspace_size(T, K, I) -> int:
+    return lib().mep_moe_layer_workspace_size(T, K, I)
+
+
+def mep_moe_layer(T, K, H, I, first, x, ids, scores, mask, w13, w2, workspace, workspace_bytes,
+                  out_bf16, out_f32, stream) -> int:
+    return lib().mep_moe_layer(T, K, H, I, first, x, ids, scores, mask, w13, w2, workspace,
+                               workspace_bytes, out_bf16, out_f32, stream)

@@ -1,0 +1,197 @@
+// 4-bit weights: codes and group scales from bf16 matrices, and their
+// layout for the experts' products (experts.h).
+//
+// Both run once, when weights are loaded; they are plain one-pass kernels.
+#include "experts.h"
+
+namespace mep {
+namespace {
+
+using namespace experts;
+
+constexpr int kPackThreads = 256;
+
+// One thread: the 32 codes that one lane of the product kernel loads at once
+// for one 16-row tile and 128 inputs: row lane % 16, and for each of the
+// chunk's four MFMAs j the 8 inputs 32 j + 8 (lane / 16) .. + 7 as one word.
+// In a word, int4 code m lies at bit 4 (m / 2) of half m % 2, so that a
+// shift and a mask leave two neighbours in the halves; 4-bit floats lie in
+// order, as the conversion instruction takes them. Rows past N and inputs
+// past K get code 0.
+__global__ __launch_bounds__(kPackThreads) void pack_codes(const uint8_t* __restrict__ codes,
+                                                           u32x4* __restrict__ out, int N, int K,
+                                                           int tiles, int KB, int fp4,
+                                                           size_t total) {
+    const size_t at = (size_t)blockIdx.x * kPackThreads + threadIdx.x;
+    if (at >= total) return;
+    const int lane = (int)(at & 63);
+    const size_t blk = at >> 6;
+    const int kb = (int)(blk % KB);
+    const size_t et = blk / KB;
+    const int row = (int)(et % tiles) * kTile + (lane & 15);
+    const size_t e = et / tiles;
+    u32x4 o = {0, 0, 0, 0};
+    if (row < N) {
+        const uint8_t* src = codes + (e * N + row) * (size_t)K;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int k = kb * kChunk + j * 32 + (lane >> 4) * 8;
+            uint32_t w = 0;
+            for (int m = 0; m < 8; ++m) {
+                const uint32_t q = k + m < K ? src[k + m] & 15u : 0u;
+                w |= q << (fp4 ? 4 * m : 4 * (m >> 1) + 16 * (m & 1));
+            }
+            o[j] = w;
+        }
+    }
+    out[at] = o;
+}
+
+// [E,N,G] -> [E][tile][superblock][4 row quads][512 / group][4 rows]; places
+// past N or the last group hold zero.
+template <typename T>
+__global__ __launch_bounds__(kPackThreads) void pack_groups(const T* __restrict__ src,
+                                                            T* __restrict__ out, int N, int G,
+                                                            int tiles, int KS, int per,
+                                                            size_t total) {
+    const size_t at = (size_t)blockIdx.x * kPackThreads + threadIdx.x;
+    if (at >= total) return;
+    size_t r = at;
+    const int i = (int)(r & 3);
+    r >>= 2;
+    const int gi = (int)(r % per);
+    r /= per;
+    const int quad = (int)(r & 3);
+    r >>= 2;
+    const int ks = (int)(r % KS);
+    r /= KS;
+    const int row = (int)(r % tiles) * kTile + quad * 4 + i;
+    const size_t e = r / tiles;
+    const int g = ks * per + gi;
+    out[at] = row < N && g < G ? src[(e * N + row) * (size_t)G + g] : (T)0;
+}
+
+// Symmetric quantization of one group per wave: s = amax / 7 (int4) or
+// amax / 6 (4-bit float) rounded to the scale's type, codes the nearest of
+// fl(w / s), ties to even.
+__global__ __launch_bounds__(kPackThreads) void quant_groups(const uint16_t* __restrict__ w,
+                                                             uint8_t* __restrict__ codes,
+                                                             uint16_t* __restrict__ scales, int K,
+                                                             int group, int G, int fp4, int f16,
+                                                             size_t total) {
+    const size_t at = (size_t)blockIdx.x * (kPackThreads / kWave) + threadIdx.x / kWave;
+    if (at >= total) return;
+    const int lane = lane_id();
+    const size_t row = at / G;
+    const int k0 = (int)(at % G) * group;
+    float v[2], amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int o = lane + i * kWave;
+        const bool in = o < group && k0 + o < K;
+        v[i] = in ? __uint_as_float((uint32_t)w[row * K + k0 + o] << 16) : 0.0f;
+        amax = fmaxf(amax, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m, kWave));
+    const float s32 = amax / (fp4 ? 6.0f : 7.0f);
+    float s;
+    uint16_t bits;
+    if (f16) {
+        const _Float16 h = (_Float16)s32;
+        bits = __builtin_bit_cast(uint16_t, h);
+        s = (float)h;
+    } else {
+        bits = (uint16_t)bf16x2_bits(s32, 0.0f);
+        s = __uint_as_float((uint32_t)bits << 16);
+    }
+    if (lane == 0) scales[at] = bits;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int o = lane + i * kWave;
+        if (o >= group || k0 + o >= K) continue;
+        const float x = s > 0.0f ? v[i] / s : 0.0f;
+        uint32_t q;
+        if (fp4) {
+            const float a = fabsf(x);
+            q = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) +
+                (a >= 3.5f) + (a > 5.0f);
+            if (q && x < 0.0f) q |= 8u;
+        } else {
+            q = (uint32_t)((int)fminf(fmaxf(__builtin_rintf(x), -8.0f), 7.0f) + 8);
+        }
+        codes[row * K + k0 + o] = (uint8_t)q;
+    }
+}
+
+bool sizes_ok(int E, int N, int K) {
+    return E >= 1 && E <= kMaxExperts && N >= 1 && N <= (1 << 20) && K >= 8 && K <= 65536 &&
+           K % 8 == 0;
+}
+
+bool group_ok(int g) { return g == 32 || g == 64 || g == 128; }
+
+size_t tiles_of(int N) { return ((size_t)N + kTile - 1) / kTile; }
+
+dim3 blocks(size_t n, int per) { return dim3((unsigned)((n + per - 1) / per)); }
+
+}  // namespace
+}  // namespace mep
+
+using namespace mep;
+using namespace mep::experts;
+
+extern "C" size_t mep_packed_code_bytes(int E, int N, int K) {
+    if (!sizes_ok(E, N, K)) return 0;
+    return (size_t)E * tiles_of(N) * ((K + kChunk - 1) / kChunk) * 1024;
+}
+
+extern "C" size_t mep_packed_scale_count(int E, int N, int K, int group) {
+    if (!sizes_ok(E, N, K) || !group_ok(group)) return 0;
+    return (size_t)E * tiles_of(N) * ((K + 511) / 512) * 16 * (512 / group);
+}
+
+extern "C" int mep_pack_weights(int E, int N, int K, int kind, int group, const uint8_t* codes,
+                                const void* scales, const uint8_t* zeros, void* packed_codes,
+                                void* packed_scales, uint8_t* packed_zeros, void* stream) {
+    if (!sizes_ok(E, N, K)) return MEP_ERR_SHAPE;
+    if ((kind != MEP_WEIGHT_INT4 && kind != MEP_WEIGHT_FP4) || !group_ok(group) ||
+        (zeros != nullptr) != (packed_zeros != nullptr) || (zeros && kind != MEP_WEIGHT_INT4))
+        return MEP_ERR_PARAM;
+    if (!codes || !scales || !packed_codes || !packed_scales) return MEP_ERR_NULLPTR;
+    if (!rows::aligned16(packed_codes) || !rows::aligned16(packed_scales) ||
+        (packed_zeros && !rows::aligned16(packed_zeros)) || ((uintptr_t)scales & 1u))
+        return MEP_ERR_SHAPE;
+    hipStream_t s = (hipStream_t)stream;
+    const int tiles = (int)tiles_of(N), KB = (K + kChunk - 1) / kChunk, KS = (K + 511) / 512;
+    const int G = (K + group - 1) / group, per = 512 / group;
+    const size_t nc = (size_t)E * tiles * KB * 64;
+    const size_t ns = mep_packed_scale_count(E, N, K, group);
+    hipLaunchKernelGGL(pack_codes, blocks(nc, kPackThreads), dim3(kPackThreads), 0, s, codes,
+                       (u32x4*)packed_codes, N, K, tiles, KB, kind == MEP_WEIGHT_FP4 ? 1 : 0, nc);
+    hipLaunchKernelGGL(pack_groups<uint16_t>, blocks(ns, kPackThreads), dim3(kPackThreads), 0, s,
+                       (const uint16_t*)scales, (uint16_t*)packed_scales, N, G, tiles, KS, per, ns);
+    if (zeros)
+        hipLaunchKernelGGL(pack_groups<uint8_t>, blocks(ns, kPackThreads), dim3(kPackThreads), 0,
+                           s, zeros, packed_zeros, N, G, tiles, KS, per, ns);
+    MEP_LAUNCH_CHECK();
+    return MEP_OK;
+}
+
+extern "C" int mep_quant_weights(int E, int N, int K, int kind, int group, int scale_dtype,
+                                 const uint16_t* w, uint8_t* codes, void* scales, void* stream) {
+    if (!sizes_ok(E, N, K)) return MEP_ERR_SHAPE;
+    if ((kind != MEP_WEIGHT_INT4 && kind != MEP_WEIGHT_FP4) || !group_ok(group) ||
+        (scale_dtype != MEP_SCALE_BF16 && scale_dtype != MEP_SCALE_F16))
+        return MEP_ERR_PARAM;
+    if (!w || !codes || !scales) return MEP_ERR_NULLPTR;
+    if (((uintptr_t)w & 1u) || ((uintptr_t)scales & 1u)) return MEP_ERR_SHAPE;
+    const int G = (K + group - 1) / group;
+    const size_t total = (size_t)E * N * G;
+    hipLaunchKernelGGL(quant_groups, blocks(total, kPackThreads / kWave), dim3(kPackThreads), 0,
+                       (hipStream_t)stream, w, codes, (uint16_t*)scales, K, group, G,
+                       kind == MEP_WEIGHT_FP4 ? 1 : 0, scale_dtype == MEP_SCALE_F16 ? 1 : 0,
+                       total);
+    MEP_LAUNCH_CHECK();
+    return MEP_OK;
+}

@@ -1,0 +1,371 @@
+// The router's expert choice and its gradient: logits [T,E] become the
+// topk_ids and scores that the plan, the remap, the combine and the expert
+// layer take.
+//
+// Forward, per token (l widened exactly; an expert whose logit is -inf or
+// NaN is absent):
+//   s = softmax(l) over the experts present, or sigmoid(l)
+//   c = l without a bias, s + bias with one; c = -inf is never taken
+//   with n_group > 1, only the topk_group groups of the largest value are
+//   kept: a group's value is its largest c without a bias, the sum of its
+//   two largest with one
+//   ids = the K largest c, descending; ties go to the lower id
+//   w = s[ids], renormalised to sum 1 if asked, times `scale`
+// A choice next to a border must not hang on how s was rounded, so c is
+// formed and compared in fp64.
+#include <algorithm>
+
+#include "rows.h"
+
+namespace mep {
+namespace {
+
+constexpr int kRouteThreads = 256;
+constexpr int kRouteWaves = kRouteThreads / kWave;
+constexpr int kRouteMaxE = 1024;
+constexpr int kRouteMaxK = 64;  // one lane per chosen expert
+constexpr int kRouteMaxGroups = 64;
+constexpr double kRenormEps = 1e-20;  // sigmoid scores may all round to zero
+
+template <typename T>
+__device__ __forceinline__ float widen(T v);
+template <>
+__device__ __forceinline__ float widen<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float widen<uint16_t>(uint16_t v) {  // bf16 bits
+    return __uint_as_float((uint32_t)v << 16);
+}
+template <>
+__device__ __forceinline__ float widen<_Float16>(_Float16 v) { return (float)v; }
+
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ uint16_t narrow<uint16_t>(float v) {
+    return (uint16_t)bf16x2_bits(v, 0.0f);
+}
+template <>
+__device__ __forceinline__ _Float16 narrow<_Float16>(float v) { return (_Float16)v; }
+
+// A logit as it is used: +inf counts as the largest finite value, NaN as -inf.
+__device__ __forceinline__ float clean(float l) {
+    return l > -INFINITY ? fminf(l, 3.402823466e38f) : -INFINITY;
+}
+
+__device__ __forceinline__ double wave_max_d(double v) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v = fmax(v, __shfl_xor(v, m, kWave));
+    return v;
+}
+
+__device__ __forceinline__ double wave_sum_d(double v) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, kWave);
+    return v;
+}
+
+// One wave per token; lane i holds experts i, i + 64, ... (V of them).
+template <typename LT, int V, bool SIGMOID>
+__global__ __launch_bounds__(kRouteThreads) void route_rows(
+    const LT* __restrict__ logits, const float* __restrict__ bias, int n_group, int topk_group,
+    int renorm, float scale, int* __restrict__ ids, float* __restrict__ scores, int T, int E,
+    int K) {
+    __shared__ double s_c[kRouteWaves][kRouteMaxE];
+    const int lane = lane_id();
+    const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x) / kWave;
+    const int t_raw = blockIdx.x * kRouteWaves + w;
+    const int t = min(t_raw, T - 1);  // waves past T work on a real row, store nothing
+
+    float l[V];
+    double c[V];
+    float top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = v * kWave + lane;
+        l[v] = e < E ? clean(widen(logits[(size_t)t * E + min(e, E - 1)])) : -INFINITY;
+        top = fmaxf(top, l[v]);
+    }
+    top = (float)wave_max_d(top);
+    double z = 1.0;
+    if constexpr (!SIGMOID) {
+        double part = 0.0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            part += l[v] > -INFINITY ? exp((double)l[v] - (double)top) : 0.0;
+        z = wave_sum_d(part);
+    }
+    auto score = [&](float x) {
+        return SIGMOID ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)top) / z;
+    };
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = v * kWave + lane;
+        c[v] = -INFINITY;
+        if (l[v] > -INFINITY) c[v] = bias ? score(l[v]) + (double)bias[e] : (double)l[v];
+        if (!(c[v] > -INFINITY)) c[v] = -INFINITY;  // a NaN bias
+    }
+
+    if (n_group > 1) {
+        const int per = E / n_group;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v * kWave + lane < E) s_c[w][v * kWave + lane] = c[v];
+        __syncthreads();
+        double a = -INFINITY, b = -INFINITY;  // the group's two largest
+        if (lane < n_group)
+            for (int i = 0; i < per; ++i) {
+                const double x = s_c[w][lane * per + i];
+                b = fmax(b, fmin(a, x));
+                a = fmax(a, x);
+            }
+        const double gv = bias && b > -INFINITY ? a + b : a;
+        int rank = 0;
+        for (int j = 0; j < n_group; ++j) {
+            const double o = __shfl(gv, j, kWave);
+            rank += o > gv || (o == gv && j < lane);
+        }
+        const uint64_t keep = __ballot(lane < n_group && rank < topk_group);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = min(v * kWave + lane, E - 1);
+            if (!((keep >> (e / per)) & 1)) c[v] = -INFINITY;
+        }
+    }
+
+    int my_id = -1;
+    float my_l = -INFINITY;
+    for (int k = 0; k < K; ++k) {
+        double best = -INFINITY;
+        int at = 0x7fffffff;
+        float bl = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (c[v] > best) { best = c[v]; at = v * kWave + lane; bl = l[v]; }
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1) {
+            const double ob = __shfl_xor(best, m, kWave);
+            const int oa = __shfl_xor(at, m, kWave);
+            const float ol = __shfl_xor(bl, m, kWave);
+            if (ob > best || (ob == best && oa < at)) { best = ob; at = oa; bl = ol; }
+        }
+        if (!(best > -INFINITY)) break;  // none left: the rest stay -1
+        if (lane == k) { my_id = at; my_l = bl; }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (at == v * kWave + lane) c[v] = -INFINITY;
+    }
+
+    double s = 0.0;
+    if (my_id >= 0) {
+        // a renormalised softmax is the softmax of the chosen
+        s = !SIGMOID && renorm ? exp((double)my_l - (double)top) : score(my_l);
+    }
+    if (renorm) {
+        if (!SIGMOID) {
+            const double m = wave_max_d(my_id >= 0 ? (double)my_l : -INFINITY);
+            s = my_id >= 0 ? exp((double)my_l - m) : 0.0;
+            const double d = wave_sum_d(s);
+            s = d > 0.0 ? s / d : 0.0;
+        } else {
+            s = s / (wave_sum_d(s) + kRenormEps);
+        }
+    }
+    if (t_raw < T && lane < K) {
+        ids[(size_t)t * K + lane] = my_id;
+        scores[(size_t)t * K + lane] = (float)(s * (double)scale);
+    }
+}
+
+// Gradient of the scores with respect to the logits. With d = dscores:
+//   g = scale * d[j], renormalised: (g_j - sum_i g_i w_i) / (sum s + eps)
+//   sigmoid           dl[j] = g_j s_j (1 - s_j) at the chosen, 0 elsewhere
+//   softmax renorm    dl[j] = w_j (g_j - sum_i g_i w_i) at the chosen
+//   softmax           dl[e] = s_e ((chosen: g_e) - sum_i g_i s_i) everywhere
+template <typename LT, int V, bool SIGMOID>
+__global__ __launch_bounds__(kRouteThreads) void route_grad_rows(
+    const LT* __restrict__ logits, const int* __restrict__ ids, const float* __restrict__ dscores,
+    int renorm, float scale, LT* __restrict__ dlogits, int T, int E, int K) {
+    const int lane = lane_id();
+    const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x) / kWave;
+    const int t = blockIdx.x * kRouteWaves + w;
+    if (t >= T) return;
+    const LT* row = logits + (size_t)t * E;
+    int id = lane < K ? ids[(size_t)t * K + lane] : -1;
+    if ((unsigned)id >= (unsigned)E) id = -1;
+    const float lj = id >= 0 ? clean(widen(row[id])) : -INFINITY;
+    const bool live = lj > -INFINITY;
+    double g = live ? (double)dscores[(size_t)t * K + lane] * (double)scale : 0.0;
+
+    float l[V];
+    double top = 0.0, z = 1.0, dot = 0.0, dl = 0.0;
+    const bool dense = !SIGMOID && !renorm;
+    if (dense) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = v * kWave + lane;
+            l[v] = e < E ? clean(widen(row[min(e, E - 1)])) : -INFINITY;
+            m = fmaxf(m, l[v]);
+        }
+        top = wave_max_d(m);
+        double part = 0.0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) part += l[v] > -INFINITY ? exp((double)l[v] - top) : 0.0;
+        z = wave_sum_d(part);
+        const double s = live ? exp((double)lj - top) / z : 0.0;
+        dot = wave_sum_d(g * s);
+        dl = s * g;
+    } else if (SIGMOID) {
+        const double x = live ? exp(-fabs((double)lj)) : 0.0;  // s(1-s) = x / (1+x)^2
+        const double s = live ? (lj >= 0.0f ? 1.0 : x) / (1.0 + x) : 0.0;
+        const double ds = x / ((1.0 + x) * (1.0 + x));
+        if (renorm) {
+            const double d = wave_sum_d(s) + kRenormEps;
+            const double gw = wave_sum_d(g * (s / d));
+            g = (g - gw) / d;
+        }
+        dl = live ? g * ds : 0.0;
+    } else {
+        const double m = wave_max_d(live ? (double)lj : -INFINITY);
+        const double x = live ? exp((double)lj - m) : 0.0;
+        const double d = wave_sum_d(x);
+        const double wj = d > 0.0 ? x / d : 0.0;
+        const double gw = wave_sum_d(g * wj);
+        dl = wj * (g - gw);
+    }
+
+    double out[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        out[v] = 0.0;
+        if (dense && l[v] > -INFINITY) out[v] = -dot * (exp((double)l[v] - top) / z);
+    }
+    for (int k = 0; k < K; ++k) {  // in k order: an id given twice adds up
+        const int at = __shfl(id, k, kWave);
+        const double d = __shfl(dl, k, kWave);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (at == v * kWave + lane) out[v] += d;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = v * kWave + lane;
+        if (e < E) dlogits[(size_t)t * E + e] = narrow<LT>((float)out[v]);
+    }
+}
+
+template <typename LT, int V>
+void launch_route(hipStream_t s, bool sig, const void* logits, const float* bias, int ng, int tg,
+                  int renorm, float scale, int* ids, float* scores, int T, int E, int K) {
+    const dim3 g((T + kRouteWaves - 1) / kRouteWaves), b(kRouteThreads);
+    if (sig)
+        hipLaunchKernelGGL((route_rows<LT, V, true>), g, b, 0, s, (const LT*)logits, bias, ng, tg,
+                           renorm, scale, ids, scores, T, E, K);
+    else
+        hipLaunchKernelGGL((route_rows<LT, V, false>), g, b, 0, s, (const LT*)logits, bias, ng, tg,
+                           renorm, scale, ids, scores, T, E, K);
+}
+
+template <typename LT>
+void dispatch_route(hipStream_t s, bool sig, const void* logits, const float* bias, int ng, int tg,
+                    int renorm, float scale, int* ids, float* scores, int T, int E, int K) {
+    if (E <= 256)
+        launch_route<LT, 4>(s, sig, logits, bias, ng, tg, renorm, scale, ids, scores, T, E, K);
+    else if (E <= 512)
+        launch_route<LT, 8>(s, sig, logits, bias, ng, tg, renorm, scale, ids, scores, T, E, K);
+    else
+        launch_route<LT, 16>(s, sig, logits, bias, ng, tg, renorm, scale, ids, scores, T, E, K);
+}
+
+template <typename LT, int V>
+void launch_route_grad(hipStream_t s, bool sig, const void* logits, const int* ids,
+                       const float* ds, int renorm, float scale, void* dl, int T, int E, int K) {
+    const dim3 g((T + kRouteWaves - 1) / kRouteWaves), b(kRouteThreads);
+    if (sig)
+        hipLaunchKernelGGL((route_grad_rows<LT, V, true>), g, b, 0, s, (const LT*)logits, ids, ds,
+                           renorm, scale, (LT*)dl, T, E, K);
+    else
+        hipLaunchKernelGGL((route_grad_rows<LT, V, false>), g, b, 0, s, (const LT*)logits, ids, ds,
+                           renorm, scale, (LT*)dl, T, E, K);
+}
+
+template <typename LT>
+void dispatch_route_grad(hipStream_t s, bool sig, const void* logits, const int* ids,
+                         const float* ds, int renorm, float scale, void* dl, int T, int E, int K) {
+    if (E <= 256)
+        launch_route_grad<LT, 4>(s, sig, logits, ids, ds, renorm, scale, dl, T, E, K);
+    else if (E <= 512)
+        launch_route_grad<LT, 8>(s, sig, logits, ids, ds, renorm, scale, dl, T, E, K);
+    else
+        launch_route_grad<LT, 16>(s, sig, logits, ids, ds, renorm, scale, dl, T, E, K);
+}
+
+bool known_dtype(int d) {
+    return d == MEP_SCALE_F32 || d == MEP_SCALE_BF16 || d == MEP_SCALE_F16;
+}
+
+bool aligned_to(const void* p, int dtype) {
+    return ((uintptr_t)p & (dtype == MEP_SCALE_F32 ? 3u : 1u)) == 0;
+}
+
+}  // namespace
+}  // namespace mep
+
+using namespace mep;
+
+extern "C" int mep_route(int T, int E, int K, const void* logits, int logit_dtype,
+                         const float* bias, int scoring, int n_group, int topk_group,
+                         int renormalize, float scale, int32_t* topk_ids, float* scores,
+                         void* stream) {
+    if (T < 0 || E < 1 || E > kRouteMaxE || K < 1 || K > kRouteMaxK ||
+        (long long)T * E >= (1ll << 40) || (long long)T * K >= (1ll << 31))
+        return MEP_ERR_SHAPE;
+    if (n_group < 1 || n_group > kRouteMaxGroups || E % n_group != 0 || topk_group < 1 ||
+        topk_group > n_group || K > topk_group * (E / n_group) || !known_dtype(logit_dtype) ||
+        (scoring != MEP_SCORE_SOFTMAX && scoring != MEP_SCORE_SIGMOID) ||
+        !(scale > -3.0e38f && scale < 3.0e38f))
+        return MEP_ERR_PARAM;
+    if (T == 0) return MEP_OK;
+    if (!logits || !topk_ids || !scores) return MEP_ERR_NULLPTR;
+    if (!aligned_to(logits, logit_dtype)) return MEP_ERR_SHAPE;
+    const bool sig = scoring == MEP_SCORE_SIGMOID;
+    hipStream_t s = (hipStream_t)stream;
+    int* ids = (int*)topk_ids;
+    if (logit_dtype == MEP_SCALE_F32)
+        dispatch_route<float>(s, sig, logits, bias, n_group, topk_group, renormalize, scale, ids, scores, T, E, K);
+    else if (logit_dtype == MEP_SCALE_BF16)
+        dispatch_route<uint16_t>(s, sig, logits, bias, n_group, topk_group, renormalize, scale, ids, scores, T, E, K);
+    else
+        dispatch_route<_Float16>(s, sig, logits, bias, n_group, topk_group, renormalize, scale, ids, scores, T, E, K);
+    MEP_LAUNCH_CHECK();
+    return MEP_OK;
+}
+
+extern "C" int mep_route_grad(int T, int E, int K, const void* logits, int logit_dtype,
+                              const int32_t* topk_ids, const float* dscores, int scoring,
+                              int renormalize, float scale, void* dlogits, void* stream) {
+    if (T < 0 || E < 1 || E > kRouteMaxE || K < 1 || K > kRouteMaxK || K > E ||
+        (long long)T * E >= (1ll << 40) || (long long)T * K >= (1ll << 31))
+        return MEP_ERR_SHAPE;
+    if (!known_dtype(logit_dtype) ||
+        (scoring != MEP_SCORE_SOFTMAX && scoring != MEP_SCORE_SIGMOID) ||
+        !(scale > -3.0e38f && scale < 3.0e38f))
+        return MEP_ERR_PARAM;
+    if (T == 0) return MEP_OK;
+    if (!logits || !topk_ids || !dscores || !dlogits) return MEP_ERR_NULLPTR;
+    if (!aligned_to(logits, logit_dtype) || !aligned_to(dlogits, logit_dtype))
+        return MEP_ERR_SHAPE;
+    const bool sig = scoring == MEP_SCORE_SIGMOID;
+    hipStream_t s = (hipStream_t)stream;
+    const int* ids = (const int*)topk_ids;
+    if (logit_dtype == MEP_SCALE_F32)
+        dispatch_route_grad<float>(s, sig, logits, ids, dscores, renormalize, scale, dlogits, T, E, K);
+    else if (logit_dtype == MEP_SCALE_BF16)
+        dispatch_route_grad<uint16_t>(s, sig, logits, ids, dscores, renormalize, scale, dlogits, T, E, K);
+    else
+        dispatch_route_grad<_Float16>(s, sig, logits, ids, dscores, renormalize, scale, dlogits, T, E, K);
+    MEP_LAUNCH_CHECK();
+    return MEP_OK;
+}

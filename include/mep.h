@@ -500,6 +500,176 @@ int mep_dispatch_quant(int T, int K, int H, const uint16_t* x, const float* smoo
 int mep_group_quant(int n, int H, int msg_bytes, const int32_t* recv_pos, int n_msgs,
                     const uint8_t* recv_msgs, uint8_t* x_q, float* scales, void* stream);
 
+/* ----------------------------------------------------------------- router */
+
+/* Scores of the router: softmax over a token's experts, or each one's
+ * sigmoid. */
+enum { MEP_SCORE_SOFTMAX = 0, MEP_SCORE_SIGMOID = 1 };
+
+/*
+ * mep_route - the router's expert choice: logits to the topk_ids that
+ * mep_plan and mep_remap_prune take and the scores that mep_combine and
+ * mep_moe_layer take (the pages start from the router's output; this is the
+ * usual choice, with the group limit and the selection bias in use with
+ * balanced experts). Per token t, with l = logits[t,:] widened exactly:
+ *   an expert with l = -inf or NaN is absent (+inf counts as the largest
+ *   finite value);
+ *   s[e] = exp(l[e]) / sum over present experts, or 1 / (1 + exp(-l[e]));
+ *   c[e] = l[e] without a bias, s[e] + bias[e] with one (c = -inf or NaN:
+ *          never chosen);
+ *   n_group > 1: experts form n_group equal runs; only the topk_group runs
+ *          of the largest value stay, ties to the lower run, where a run's
+ *          value is its largest c without a bias and the sum of its two
+ *          largest c with one (a missing second counts 0);
+ *   topk_ids[t,:] = the K experts of the largest c, descending, ties to the
+ *          lower id; -1 where none is left;
+ *   scores[t,k] = scale * w[k] with w[k] = s[topk_ids[t,k]], 0 for -1;
+ *          with renormalize, w is the softmax of the chosen logits, or
+ *          s[k] / (sum of the chosen s + 1e-20).
+ * c is formed and compared in fp64, so the choice does not hang on the
+ * rounding of s. Note that mep_plan needs ids in [0, E): with fewer than K
+ * experts present use mep_moe_layer or a send map, which skip -1.
+ *   logits [T,E] of logit_dtype (MEP_SCALE_*), bias [E] fp32 or NULL,
+ *   topk_ids [T,K] int32, scores [T,K] fp32.
+ * Sizes: T >= 0 (0 does nothing), 1 <= E <= 1024, 1 <= K <= 64,
+ * T*K < 2^31, T*E < 2^40.
+ * Errors: MEP_ERR_NULLPTR, MEP_ERR_PARAM (n_group not in [1, 64] or no
+ * divisor of E, topk_group not in [1, n_group], K above the experts that the
+ * kept groups hold, unknown dtype or scoring, scale not finite),
+ * MEP_ERR_SHAPE, MEP_ERR_HIP.
+ */
+int mep_route(int T, int E, int K, const void* logits, int logit_dtype, const float* bias,
+              int scoring, int n_group, int topk_group, int renormalize, float scale,
+              int32_t* topk_ids, float* scores, void* stream);
+
+/*
+ * mep_route_grad - gradient of mep_route's scores with respect to the
+ * logits, the ids held fixed (the bias only steers the choice and gets
+ * none). With g[k] = scale * dscores[t,k] at the ids in [0, E) (0 at others)
+ * and s, w as above:
+ *   sigmoid: a[k] = g[k], or with renormalize
+ *            (g[k] - sum_i g[i] w[i]) / (sum_i s[i] + 1e-20);
+ *            dl[id] = a[k] s (1 - s), 0 at experts not chosen
+ *   softmax: dl[e] = s[e] (sum of g[k] with id e - sum_i g[i] s[i]) for
+ *            every present expert, or with renormalize
+ *            dl[id] = w[k] (g[k] - sum_i g[i] w[i]), 0 elsewhere
+ * An id given twice in a row adds up. Computed in fp64, rounded once to
+ * logit_dtype. The whole of dlogits [T,E] is written; it may not overlap
+ * the inputs. K <= E; other sizes and errors as mep_route.
+ */
+int mep_route_grad(int T, int E, int K, const void* logits, int logit_dtype,
+                   const int32_t* topk_ids, const float* dscores, int scoring, int renormalize,
+                   float scale, void* dlogits, void* stream);
+
+/* -------------------------------------------------- experts, few tokens */
+
+/* Weight kinds: bf16 rows; 4-bit integers (code - 8, or code - zero point)
+ * and 4-bit floats (sign, two exponent bits, one mantissa bit: 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6) with one scale per row and group of inputs. */
+enum { MEP_WEIGHT_BF16 = 0, MEP_WEIGHT_INT4 = 1, MEP_WEIGHT_FP4 = 2 };
+
+/*
+ * A set of E matrices [N, K] (K the inputs). The struct is read on the host
+ * during the call; its pointers are device pointers.
+ *   MEP_WEIGHT_BF16: data = [E,N,K] bf16, scales = zeros = NULL.
+ *   MEP_WEIGHT_INT4, MEP_WEIGHT_FP4: data, scales and (INT4 only, may be
+ *   NULL) zeros as mep_pack_weights wrote them; group in {32, 64, 128};
+ *   scale_dtype MEP_SCALE_BF16 or MEP_SCALE_F16.
+ * All 16-byte aligned. 1 <= E <= 1024, 1 <= N <= 2^20, 8 <= K <= 65536,
+ * K % 8 == 0.
+ */
+typedef struct {
+    int kind, E, N, K, group, scale_dtype;
+    const void* data;
+    const void* scales;
+    const uint8_t* zeros;
+} mep_weights;
+
+/* Bytes of mep_pack_weights' packed_codes, and elements of packed_scales
+ * (and bytes of packed_zeros). Host only; 0 for unsupported sizes. */
+size_t mep_packed_code_bytes(int E, int N, int K);
+size_t mep_packed_scale_count(int E, int N, int K, int group);
+
+/*
+ * mep_pack_weights - lays 4-bit weights out for mep_expert_matvec and
+ * mep_moe_layer; once, when they are loaded.
+ *   codes  [E,N,K] uint8, one code each in the low four bits;
+ *   scales [E,N,G] 16-bit floats, G = ceil(K / group), group i of a row
+ *          covering inputs i*group and on;
+ *   zeros  [E,N,G] uint8 (INT4: the value of code q is (q - zero) * scale;
+ *          without them (q - 8) * scale), NULL together with packed_zeros.
+ * Errors: MEP_ERR_NULLPTR, MEP_ERR_PARAM (kind, group, zeros unpaired or
+ * with FP4), MEP_ERR_SHAPE (sizes, alignment), MEP_ERR_HIP.
+ */
+int mep_pack_weights(int E, int N, int K, int kind, int group, const uint8_t* codes,
+                     const void* scales, const uint8_t* zeros, void* packed_codes,
+                     void* packed_scales, uint8_t* packed_zeros, void* stream);
+
+/*
+ * mep_quant_weights - codes and scales (as mep_pack_weights takes them) of
+ * bf16 matrices, symmetric, per row and group:
+ *   scale = fl(max |w| / 7) (INT4) or fl(max |w| / 6) (FP4) rounded to
+ *           scale_dtype (MEP_SCALE_BF16 or MEP_SCALE_F16)
+ *   code  = the nearest to fl(w / scale), ties to even; INT4 clamped to
+ *           [-8, 7] and stored plus 8; FP4 clamped to +-6; zero where
+ *           scale == 0
+ * w [E,N,K] bf16, finite. Errors as mep_pack_weights.
+ */
+int mep_quant_weights(int E, int N, int K, int kind, int group, int scale_dtype,
+                      const uint16_t* w, uint8_t* codes, void* scales, void* stream);
+
+/*
+ * mep_expert_matvec - products of a few rows with 4-bit matrices, each
+ * route's own:
+ *   out[t,r,:] = W[ids[t*R+r] - first] x[t,:]       (x_per_route == 0)
+ *   out[t,r,:] = W[ids[t*R+r] - first] x[t,r,:]     (x_per_route != 0)
+ * fp32 accumulation, rounded once. A route whose index is outside [0, E) or
+ * whose mask byte is 0 leaves its row of out untouched. With ids == NULL
+ * out[t,:] = W[0] x[t,:] (then E == 1, R is not read, and mask, x_per_route
+ * and first are 0).
+ *   x bf16, 16-byte aligned; ids [T*R] int32; mask [T*R] uint8 or NULL;
+ *   exactly one of out_bf16, out_f32, [T,R,N].
+ * T >= 0 (0 does nothing); at most 2048 routes. MEP_WEIGHT_BF16 is refused
+ * (those products are a library's).
+ * Errors: MEP_ERR_NULLPTR, MEP_ERR_PARAM, MEP_ERR_SHAPE, MEP_ERR_HIP.
+ */
+int mep_expert_matvec(int T, int R, int first, const uint16_t* x, int x_per_route,
+                      const int32_t* ids, const uint8_t* mask, const mep_weights* w,
+                      uint16_t* out_bf16, float* out_f32, void* stream);
+
+/* Bytes of device workspace mep_moe_layer needs; 0 if unsupported. */
+size_t mep_moe_layer_workspace_size(int T, int K, int I);
+
+/*
+ * mep_moe_layer - the whole expert layer for a few tokens (a decode step),
+ * without dispatch and combine around it:
+ *   h[t,k] = silu(Wg x[t]) * (Wu x[t])      with W13 = [Wg; Wu] of the expert
+ *   out[t] = sum over live k of scores[t*K+k] * (W2 h[t,k])
+ * silu(v) = v / (1 + exp(-v)). A route is live if e = ids[t*K+k] - first is
+ * in [0, E) (the experts held here, as mep_remap_prune's ids, of which rank
+ * r holds place_per_rank from r*place_per_rank on; or rows of a [E+B, H, H']
+ * weight tensor as mep_plan_weight_rows names them) and its mask byte (its
+ * balanced_mask) is not 0; a token without one gets a zero row. Sums are
+ * fp32; between the two kernels h keeps 24 bits of mantissa when out_f32 is
+ * given and 16 when not; the output is rounded once. Every sum has a fixed order.
+ *   x [T,H] bf16; ids [T*K] int32; scores [T*K] fp32; mask [T*K] uint8 or
+ *   NULL; w13 [E, 2I, H] and w2 [E, H, I] of one kind, group and scale type;
+ *   out_bf16, out_f32 [T,H], either may be NULL but not both; workspace of
+ *   mep_moe_layer_workspace_size() bytes, 256-byte aligned, contents on
+ *   entry do not matter, clobbered (calls that may overlap, replays of
+ *   captured graphs among them, need one each).
+ * Sizes: 0 <= T <= 128 (0 does nothing; beyond, dispatch and combine
+ * around the experts' full products are the better path), K >= 1,
+ * T*K <= 2048, 8 <= H, I <= 65536, multiples of 8. Row pointers 16-byte
+ * aligned.
+ * Errors: MEP_ERR_NULLPTR, MEP_ERR_PARAM (weights that do not match each
+ * other, workspace too small or misaligned), MEP_ERR_SHAPE, MEP_ERR_HIP.
+ */
+int mep_moe_layer(int T, int K, int H, int I, int first, const uint16_t* x, const int32_t* ids,
+                  const float* scores, const uint8_t* mask, const mep_weights* w13,
+                  const mep_weights* w2, void* workspace, size_t workspace_bytes,
+                  uint16_t* out_bf16, float* out_f32, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
