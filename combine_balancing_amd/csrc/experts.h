@@ -3,17 +3,24 @@
 // weights are read once per expert that any route reaches; everything else
 // is small, so the kernels stream weights and are bound by HBM.
 //
-// Products run on the matrix cores, one 16x16x32 bf16 MFMA per 16 weight
-// rows, 32 inputs and up to 16 routes: its operands are 16 bytes of a weight
-// row per lane and 16 bytes of a route's input per lane, so any route count
-// up to 16 costs the same weight traffic, and columns of different routes
-// never mix (a NaN in one route's input stays in its column). Accumulation
-// is fp32.
-//
-// Lane layout of that MFMA (i = lane % 16, q = lane / 16): A holds row i,
-// inputs 8q..8q+7; B holds column i, the same inputs; C holds column i, rows
-// 4q..4q+3.
+// Products run on the matrix cores (16x16x32 bf16 MFMA, fp32 sums): columns
+// are routes, so a route's products never mix with another's and a NaN in
+// one stays there. The MFMA wants lane l (i = l % 16, q = l / 16) to hold
+// row i, inputs 8q..8q+7 of A and column i, the same inputs, of B. Loading
+// 16 weight rows like that touches 64 bytes of a row per instruction, and
+// such reads reached 5.4-6.0 TB/s where whole 128-byte lines reach 7.1. So
+// an MFMA here takes 8 rows and 64 inputs: lanes i < 8 hold row i and the
+// first 32 inputs, lanes i >= 8 row i - 8 and the other 32, and B likewise
+// holds 8 routes, the first 32 inputs in columns 0-7 and the other 32 in
+// columns 8-15. Of the 16x16 results the blocks (rows 0-7, columns 0-7) and
+// (rows 8-15, columns 8-15) are the two halves of the wanted 8x8 sums, the
+// other two mean nothing. Lane l's four results are rows 4q..4q+3 of column
+// i; the second half of lane l's sum lies in lane l + 40. Up to 8 routes
+// cost one MFMA per KiB of weights this way, and 16 columns are not half
+// idle when few routes share an expert.
 #pragma once
+
+#include <utility>
 
 #include "rows.h"
 
@@ -26,11 +33,34 @@ using rows::u32x4;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kTile = 16;       // weight rows of one MFMA
-constexpr int kChunk = 128;     // inputs of one load step: four MFMAs
+// Register arrays that a lambda captures stay registers only if it is inlined.
+#define MEP_INLINE __attribute__((always_inline))
+
+// f(0), f(1), .. f(N - 1) with constant arguments, up to the first that
+// returns true; whether one did.
+template <class F, int... I>
+__device__ __forceinline__ bool any_of(F f, std::integer_sequence<int, I...>) {
+    return (f(std::integral_constant<int, I>{}) || ...);
+}
+template <int N, class F>
+__device__ __forceinline__ bool any_of(F f) {
+    return any_of(f, std::make_integer_sequence<int, N>{});
+}
+
+constexpr int kTile = 8;        // weight rows of one MFMA
+constexpr int kStep = 64;       // inputs of one MFMA
+constexpr int kCols = 8;        // routes of one MFMA
+constexpr int kPackK = 256;     // inputs of one packed 4-bit block
 constexpr int kMaxRoutes = 2048;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxLayerTokens = 128;
+constexpr int kMaxWaves = 16;
+#ifndef DN_WPE
+#define DN_WPE 1
+#endif
+#ifndef RD_WPE
+#define RD_WPE 1
+#endif
 
 // Routed list that the layer's first kernel leaves for its second.
 struct Table {
@@ -46,9 +76,8 @@ struct Weights {
     const uint8_t* zeros;
     int N, K;
     int KV;     // K / 8, inputs in vectors of 8
-    int tiles;  // packed: ceil(N / 16)
-    int KB;     // ceil(K / 128)
-    int KS;     // packed: ceil(K / 512), superblocks of scales
+    int tiles;  // packed: ceil(N / 8)
+    int KB;     // packed: ceil(K / 256)
 };
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
@@ -56,56 +85,84 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
+// Loads from a buffer (its base and size in scalar registers) at a scalar
+// offset plus a byte offset per lane: stepping through it costs no vector
+// instruction, and a load past its end returns 0. `kNt` streams past the
+// caches (weights are used once).
+typedef __amdgpu_buffer_rsrc_t Buffer;
+constexpr int kNt = 2;
+
+__device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00027000);
+}
+template <typename T, int AUX>
+__device__ __forceinline__ T buffer_load(Buffer b, uint32_t lane_bytes, uint32_t bytes) {
+    if constexpr (sizeof(T) == 16)
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b128(b, lane_bytes, bytes, AUX));
+    else if constexpr (sizeof(T) == 8)
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b64(b, lane_bytes, bytes, AUX));
+    else
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(b, lane_bytes, bytes, AUX));
+}
+
+// Vector (8 inputs) of a 64-input step that a lane holds: q, or q + 4 in the
+// lanes of the second half.
+__device__ __forceinline__ int lane_vec(int lane) { return (lane >> 4) + ((lane >> 3) & 1) * 4; }
+
 // ---------------------------------------------------------------- weights
 //
-// A weight kind gives: Ptr (where a lane's part of one 16-row tile starts),
-// Reg (one chunk of it in registers), load, and mma (chunk times NTB column
-// blocks, each the sum of NX input terms).
+// A weight kind gives: kSteps (MFMA steps of one chunk), Ptr (where a lane's
+// part of one 8-row tile starts), Reg (one chunk of it in registers), load,
+// and mma (chunk times NB column blocks).
 
 struct Bf16Weights {
-    struct Ptr {
-        const u32x4* p;
-    };
+    static constexpr int kSteps = 2;
+    static constexpr int kMaxHeld = 4;  // chunks of inputs that a wave can hold
     struct Reg {
-        u32x4 a[4];
+        u32x4 a[kSteps];
     };
-    static __device__ __forceinline__ Ptr at(const Weights& w, int e, int row0, int lane) {
-        const int row = min(row0 + (lane & 15), w.N - 1);
-        return {w.codes + ((size_t)e * w.N + row) * w.KV + (lane >> 4)};
+    struct Ptr {
+        Buffer rows;
+    };
+    struct Lane {
+        uint32_t vec, bytes;
+    };
+    static __device__ __forceinline__ Lane lane_of(const Weights& w, int lane) {
+        const uint32_t v = lane_vec(lane);
+        return {v, (uint32_t)((lane & 7) * w.KV + v) * 16u};
     }
-    static __device__ __forceinline__ void load(Reg& r, const Ptr& p, const Weights& w, int c,
-                                                int lane) {
-        if (c * 16 + 16 <= w.KV) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r.a[j] = __builtin_nontemporal_load(p.p + c * 16 + j * 4);
-        } else {  // the last, cut chunk: inputs past K count as zero on both sides
-            const int q = lane >> 4;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int v = c * 16 + j * 4 + q;
-                const u32x4 a = p.p[min(v, w.KV - 1) - q];
-                r.a[j] = v < w.KV ? a : u32x4{0, 0, 0, 0};
-            }
-        }
+    static __device__ __forceinline__ Ptr at(const Weights& w, int e, int row0) {
+        const u32x4* p = w.codes + ((size_t)e * w.N + min(row0, w.N - kTile)) * w.KV;
+        return {buffer_of(p, (uint32_t)(kTile * w.KV) * 16u)};
     }
-    template <int NT, int NTB, int NX>
-    static __device__ __forceinline__ void mma(const Reg (&r)[NT], const u32x4 (&x)[NTB][NX][4],
-                                               f32x4 (&acc)[NT][NTB]) {
+    static __device__ __forceinline__ void load(Reg& r, const Ptr& p, const Lane& l, int c) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kSteps; ++j)
+            r.a[j] = buffer_load<u32x4, kNt>(p.rows, l.bytes + j * 128, c * (kSteps * 128));
+    }
+    // The chunk that K cuts: a lane's vectors past it hold the next row.
+    static __device__ __forceinline__ void cut(Reg& r, const Lane& l, const Weights& w, int c) {
 #pragma unroll
-            for (int b = 0; b < NTB; ++b)
+        for (int j = 0; j < kSteps; ++j)
+            if ((c * kSteps + j) * 8 + (int)l.vec >= w.KV) r.a[j] = u32x4{0, 0, 0, 0};
+    }
+    template <int NT, int NB>
+    static __device__ __forceinline__ void mma(const Reg (&r)[NT], const u32x4 (&x)[NB][kSteps],
+                                               f32x4 (&acc)[NT][NB]) {
 #pragma unroll
-                for (int n = 0; n < NX; ++n)
+        for (int j = 0; j < kSteps; ++j)
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) acc[i][b] = mfma(r[i].a[j], x[b][n][j], acc[i][b]);
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) acc[i][b] = mfma(r[i].a[j], x[b][j], acc[i][b]);
     }
 };
 
-// 4-bit codes in the packed layout (see pack_codes): 1 KiB per 16 rows and
-// 128 inputs, 16 bytes per lane in MFMA order; scales and zero points
-// [tile][superblock of 512 inputs][4 row quads][groups][4 rows], the order
-// in which the accumulator's lanes need them.
+// 4-bit codes in the packed layout (pack4.hip): 1 KiB per 8 rows and 256
+// inputs, 16 bytes per lane, one word per step; scales and zero points
+// [tile][block][2 row quads][groups][4 rows], the order in which the
+// accumulators' lanes need them (groups of 32: those of the steps' first
+// halves, then those of the second, since lanes q >= 2 hold the latter).
 //
 // An int4 code q becomes the bf16 number 128 + q by or-ing it into the
 // mantissa of 128 (one shift and one and-or per two codes). The constant is
@@ -119,39 +176,52 @@ struct Bf16Weights {
 // A 4-bit float is converted by the hardware, two codes per instruction.
 template <bool FP4, int G, bool ZP, bool F16>
 struct PackedWeights {
-    static constexpr int GP = kChunk / G;  // groups per chunk
-    static constexpr int GM = G / 32;      // MFMAs per group
+    static constexpr int kSteps = 4;
+    static constexpr int kMaxHeld = 2;
+    static constexpr int SM = G == 128 ? 2 : 1;  // steps per scale
+    static constexpr int GL = kSteps / SM;       // scales per lane, row and chunk
+    static constexpr int GP = kPackK / G;        // groups per block
     struct Ptr {
-        const u32x4* p;
-        const uint32_t* s;
-        const uint32_t* z;
+        Buffer codes, scales, zeros;
+    };
+    struct Lane {
+        uint32_t bytes, group;  // group: of the zero points, which take 1 byte a row
     };
     struct Reg {
         u32x4 a;
-        uint32_t s[GP * 2];
-        uint32_t z[ZP ? GP : 1];
+        uint32_t s[GL * 2];
+        uint32_t z[ZP ? GL : 1];
     };
-    static __device__ __forceinline__ Ptr at(const Weights& w, int e, int row0, int lane) {
-        const int np = w.tiles * kTile;
-        const int row = min(row0 + (lane & 15), np - 1);
-        const int quad = min((row0 >> 2) + (lane >> 4), np / 4 - 1);
-        const size_t tile = (size_t)e * w.tiles + (row >> 4);
-        const size_t qt = (size_t)e * w.tiles + (quad >> 2);
-        const size_t group0 = (qt * w.KS * 4 + (quad & 3)) * (512 / G);  // in quads of rows
-        return {w.codes + tile * w.KB * 64 + (lane >> 4) * 16 + (row & 15),
-                (const uint32_t*)w.scales + group0 * 2, (const uint32_t*)w.zeros + group0};
+    static __device__ __forceinline__ Lane lane_of(const Weights&, int lane) {
+        return {(uint32_t)lane * 16u,
+                (uint32_t)(((lane >> 4) & 1) * GP + (G == 32 ? (lane >> 5) * GL : 0)) * 4u};
     }
-    static __device__ __forceinline__ void load(Reg& r, const Ptr& p, const Weights&, int c,
-                                                int) {
-        r.a = __builtin_nontemporal_load(p.p + (size_t)c * 64);
-        const int g = (c >> 2) * (4 * (512 / G)) + (c & 3) * GP;
+    static __device__ __forceinline__ Ptr at(const Weights& w, int e, int row0) {
+        const size_t tile = (size_t)e * w.tiles + min(row0 / kTile, w.tiles - 1);
+        const size_t g = tile * w.KB * (8 * GP);
+        const uint32_t n = (uint32_t)w.KB * (8 * GP);
+        Ptr p;
+        p.codes = buffer_of(w.codes + tile * w.KB * 64, (uint32_t)w.KB * 1024u);
+        p.scales = buffer_of(w.scales + g, n * 2u);
+        if constexpr (ZP) p.zeros = buffer_of(w.zeros + g, n);
+        return p;
+    }
+    static __device__ __forceinline__ void load(Reg& r, const Ptr& p, const Lane& l, int c) {
+        r.a = buffer_load<u32x4, kNt>(p.codes, l.bytes, c * 1024);
 #pragma unroll
-        for (int i = 0; i < GP * 2; ++i) r.s[i] = p.s[(size_t)g * 2 + i];
-        if constexpr (ZP) {
+        for (int i = 0; i < GL / 2; ++i) {
+            const u32x4 s = buffer_load<u32x4, 0>(p.scales, l.group * 2 + i * 16, c * (16 * GP));
 #pragma unroll
-            for (int i = 0; i < GP; ++i) r.z[i] = p.z[(size_t)g + i];
+            for (int k = 0; k < 4; ++k) r.s[i * 4 + k] = s[k];
+            if constexpr (ZP) {
+                const u32x2 z = buffer_load<u32x2, 0>(p.zeros, l.group + i * 8, c * (8 * GP));
+                r.z[i * 2] = z[0];
+                r.z[i * 2 + 1] = z[1];
+            }
         }
     }
+    // Codes and scales past K are zero in the layout.
+    static __device__ __forceinline__ void cut(Reg&, const Lane&, const Weights&, int) {}
     static __device__ __forceinline__ float scale(uint32_t w, int hi) {
         if constexpr (F16) {
             const uint16_t b = (uint16_t)(hi ? w >> 16 : w);
@@ -159,7 +229,15 @@ struct PackedWeights {
         }
         return __uint_as_float(hi ? w & 0xffff0000u : w << 16);
     }
-    static __device__ __forceinline__ u32x4 decode(uint32_t d) {
+    // k128: 128.0 twice. Given in a vector register, so that the mask (a
+    // scalar) and it fit one v_and_or_b32; as two constants they took two
+    // instructions.
+    static __device__ __forceinline__ uint32_t offset_bits() {
+        uint32_t k128 = 0x43004300u;
+        asm("" : "+v"(k128));
+        return k128;
+    }
+    static __device__ __forceinline__ u32x4 decode(uint32_t d, uint32_t k128) {
         u32x4 o;
         if constexpr (FP4) {
             o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 0));
@@ -168,46 +246,43 @@ struct PackedWeights {
             o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 3));
         } else {
 #pragma unroll
-            for (int p = 0; p < 4; ++p) o[p] = ((d >> (4 * p)) & 0x000f000fu) | 0x43004300u;
+            for (int p = 0; p < 4; ++p) o[p] = ((d >> (4 * p)) & 0x000f000fu) | k128;
         }
         return o;
     }
-    template <int NT, int NTB, int NX>
-    static __device__ __forceinline__ void mma(const Reg (&r)[NT], const u32x4 (&x)[NTB][NX][4],
-                                               f32x4 (&acc)[NT][NTB]) {
+    template <int NT, int NB>
+    static __device__ __forceinline__ void mma(const Reg (&r)[NT], const u32x4 (&x)[NB][kSteps],
+                                               f32x4 (&acc)[NT][NB]) {
         constexpr uint32_t kOff = ZP ? 0xc300c300u : 0xc308c308u;  // -128, -136
         const u32x4 off = {kOff, kOff, kOff, kOff};
+        const uint32_t k128 = offset_bits();
 #pragma unroll
-        for (int g = 0; g < GP; ++g) {
-            f32x4 x0[NTB];
+        for (int g = 0; g < GL; ++g) {
+            f32x4 x0[NB];
 #pragma unroll
-            for (int b = 0; b < NTB; ++b) {
+            for (int b = 0; b < NB; ++b) {
                 x0[b] = f32x4{0, 0, 0, 0};
                 if constexpr (!FP4) {
 #pragma unroll
-                    for (int j = 0; j < GM; ++j)
-#pragma unroll
-                        for (int n = 0; n < NX; ++n) x0[b] = mfma(off, x[b][n][g * GM + j], x0[b]);
+                    for (int j = 0; j < SM; ++j) x0[b] = mfma(off, x[b][g * SM + j], x0[b]);
                 }
             }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                f32x4 c[NTB];
+                f32x4 c[NB];
 #pragma unroll
-                for (int b = 0; b < NTB; ++b) c[b] = x0[b];
+                for (int b = 0; b < NB; ++b) c[b] = x0[b];
 #pragma unroll
-                for (int j = 0; j < GM; ++j) {
-                    const u32x4 a = decode(r[i].a[g * GM + j]);
+                for (int j = 0; j < SM; ++j) {
+                    const u32x4 a = decode(r[i].a[g * SM + j], k128);
 #pragma unroll
-                    for (int b = 0; b < NTB; ++b)
-#pragma unroll
-                        for (int n = 0; n < NX; ++n) c[b] = mfma(a, x[b][n][g * GM + j], c[b]);
+                    for (int b = 0; b < NB; ++b) c[b] = mfma(a, x[b][g * SM + j], c[b]);
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const float s = scale(r[i].s[g * 2 + k / 2], k & 1);
 #pragma unroll
-                    for (int b = 0; b < NTB; ++b) {
+                    for (int b = 0; b < NB; ++b) {
                         float v = c[b][k];
                         if constexpr (ZP) {
                             const float z = (float)((r[i].z[g] >> (8 * k)) & 0xffu) * (1.0f / 128);
@@ -223,68 +298,90 @@ struct PackedWeights {
 
 // ----------------------------------------------------------------- inputs
 
-// bf16 rows of K inputs, read as they are. A lane of a column past the last
-// route reads a real route's row; its column is not stored.
-struct PlainInput {
-    static constexpr int NX = 1;
-    const u32x4* p;
-    __device__ __forceinline__ void load(u32x4 (&x)[1][4], int c, int KV, int q) const {
-        if (c * 16 + 16 <= KV) {
+// A route's inputs as bf16 terms to be summed: one for bf16 rows read as they
+// are; for the layer's h (fp32) each term is the rest of the ones before,
+// rounded (two terms lose at most 2^-17 of the value, three at most 2^-25),
+// stored per 8 values as 16 bytes of each term. Two terms serve a bf16
+// output (its own rounding is 2^-8), three an fp32 one: with two, an fp32
+// output measured 2.7e-6 from the exact result where 2.5e-7 is fp32's share.
+// The terms of a route take columns of their own, kRoutes routes to a block
+// of 8 columns: column c holds term c / kRoutes of route c % kRoutes. An
+// expert rarely sees more than a few of a decode step's routes, so these
+// columns would mostly stand empty, and the terms then cost no product and
+// no load of their own. Inputs past K count as zero. The lanes of a column
+// past the last route (or term) read a real one; their column is not used.
+template <int TERMS>
+struct Input {
+    static constexpr int kRoutes = TERMS == 1 ? 8 : TERMS == 2 ? 4 : 2;
+    uint32_t bytes;  // where the lane's vector of the route's row starts
+    __device__ __forceinline__ void row(int r, int KV, int lane) {
+        const uint32_t term = min((lane & 7) / kRoutes, TERMS - 1);
+        bytes = (((uint32_t)r * KV + lane_vec(lane)) * TERMS + term) * 16u;
+    }
+    template <int STEPS>
+    __device__ __forceinline__ void load(u32x4 (&x)[STEPS], Buffer b, int c) const {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[0][j] = p[c * 16 + j * 4 + q];
-        } else {
+        for (int j = 0; j < STEPS; ++j)
+            x[j] = buffer_load<u32x4, 0>(b, bytes + j * (128 * TERMS), c * (STEPS * 128 * TERMS));
+    }
+    template <int STEPS>
+    static __device__ __forceinline__ void cut(u32x4 (&x)[STEPS], int c, int KV, int lane) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int v = c * 16 + j * 4 + q;
-                const u32x4 a = p[min(v, KV - 1)];
-                x[0][j] = v < KV ? a : u32x4{0, 0, 0, 0};
-            }
-        }
+        for (int j = 0; j < STEPS; ++j)
+            if ((c * STEPS + j) * 8 + lane_vec(lane) >= KV) x[j] = u32x4{0, 0, 0, 0};
+    }
+    // The wanted sum of a lane i < kRoutes, q < 2: both halves of the inputs
+    // and all terms.
+    static __device__ __forceinline__ float total(float v, int lane) {
+        v = v + __shfl(v, (lane + 40) & 63, kWave);
+        float o = v;
+#pragma unroll
+        for (int t = 1; t < TERMS; ++t) o = o + __shfl(v, (lane + t * kRoutes) & 63, kWave);
+        return o;
     }
 };
 
-// fp32 values held as a sum of bf16 terms, each the rest of the ones before
-// rounded (two terms lose at most 2^-17 of the value, three at most 2^-25),
-// in rows padded with zeros to whole chunks; per 8 values 16 bytes of each
-// term. Two terms serve a bf16 output (its own rounding is 2^-8), three an
-// fp32 one: with two, an fp32 output measured 2.7e-6 from the exact result
-// where 2.5e-7 is fp32's share.
-template <int TERMS>
-struct SplitInput {
-    static constexpr int NX = TERMS;
-    const u32x4* p;
-    __device__ __forceinline__ void load(u32x4 (&x)[TERMS][4], int c, int, int q) const {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int n = 0; n < TERMS; ++n) x[n][j] = p[(c * 16 + j * 4 + q) * TERMS + n];
-    }
-};
+template <class W>
+__host__ __device__ __forceinline__ int chunks(int K) {
+    return (K + W::kSteps * kStep - 1) / (W::kSteps * kStep);
+}
 
 // acc[i][b] += tile i of the weights times column block b over chunks
-// [lo, hi), with the next chunk's loads issued before a chunk is used.
-template <class W, class X, int NT, int NTB>
+// [lo, hi), the loads of the next D - 1 chunks in flight while one is used.
+// The loop has no branch around its loads: where two paths with and without
+// loads meet, the compiler waits for all of them before the next use, which
+// undoes the prefetch. So past the end the last chunk is loaded again.
+template <class W, int D, int TERMS, int NT, int NB>
 __device__ __forceinline__ void stream(const Weights& w, const typename W::Ptr (&wp)[NT],
-                                       const X (&xp)[NTB], int lo, int hi, int lane,
-                                       f32x4 (&acc)[NT][NTB]) {
-    typename W::Reg r0[NT], r1[NT];
-    u32x4 x0[NTB][X::NX][4], x1[NTB][X::NX][4];
-    const int q = lane >> 4;
-    auto load = [&](typename W::Reg (&r)[NT], u32x4 (&x)[NTB][X::NX][4], int c) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) W::load(r[i], wp[i], w, c, lane);
-#pragma unroll
-        for (int b = 0; b < NTB; ++b) xp[b].load(x[b], c, w.KV, q);
-    };
+                                       Buffer xb, const Input<TERMS> (&xp)[NB], int lo, int hi,
+                                       int lane, f32x4 (&acc)[NT][NB]) {
     if (lo >= hi) return;
-    load(r0, x0, lo);
+    typename W::Reg r[D][NT];
+    u32x4 x[D][NB][W::kSteps];
+    const typename W::Lane l = W::lane_of(w, lane);
+    auto load = [&](int d, int c) MEP_INLINE {
+        c = min(c, hi - 1);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) W::load(r[d][i], wp[i], l, c);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) xp[b].load(x[d][b], xb, c);
+    };
+    const int full = w.KV / (W::kSteps * 8);  // the chunk that K cuts, if any
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) load(d, lo + d);
     for (int c = lo;;) {
-        if (c + 1 < hi) load(r1, x1, c + 1);
-        W::template mma<NT, NTB, X::NX>(r0, x0, acc);
-        if (++c >= hi) break;
-        if (c + 1 < hi) load(r0, x0, c + 1);
-        W::template mma<NT, NTB, X::NX>(r1, x1, acc);
-        if (++c >= hi) break;
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            load((d + D - 1) % D, c + D - 1);
+            if (c == full) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) W::cut(r[d][i], l, w, c);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) Input<TERMS>::cut(x[d][b], c, w.KV, lane);
+            }
+            W::template mma<NT, NB>(r[d], x[d], acc);
+            if (++c >= hi) return;
+        }
     }
 }
 
@@ -301,49 +398,74 @@ struct RowsArgs {
     void* out;           // [n, N] bf16 or fp32
     int out_f32;
     // first half of the layer
-    u32x4* h;            // [n][Ip / 8][terms]
-    int I, Ip, terms;
+    u32x4* h;            // [n][I / 8][terms]
+    int I, terms;
     Table* table;
 };
 
-// Finds the blockIdx.y-th expert that any route reaches and its routes, in
-// route order. Returns false (for the whole work-group) past the last one.
-template <int NW>
+// The experts that any route reaches ("slots", ascending), jobs of up to 8
+// of an expert's routes, and an expert's routes in route order. All threads
+// of the work-group take part in each call.
 struct Finder {
-    uint32_t bits[kMaxExperts / 32];
-    int count[NW], less[NW];
     int16_t id[kMaxRoutes];
     uint16_t list[kMaxRoutes];
+    uint16_t routes[kMaxExperts];  // of each expert
+    uint16_t job[kMaxRoutes];      // its expert; a job's place among its expert's
+    uint8_t pass[kMaxRoutes];      // jobs, 8 routes each
+    int count[kMaxWaves], less[kMaxWaves], slots, jobs;
 
-    __device__ __forceinline__ bool find(const RowsArgs& a, int slot, int* e_out, int* cnt_out,
-                                         int* off_out, int* total_out) {
-        const int tid = threadIdx.x, lane = lane_id();
-        const int wave = __builtin_amdgcn_readfirstlane(tid) / kWave;
-        if (tid < kMaxExperts / 32) bits[tid] = 0u;
+    // Reads the ids; returns the number of jobs.
+    __device__ __forceinline__ int begin(const RowsArgs& a) {
+        const int tid = threadIdx.x;
+        // counted in pairs of 16 bits: no more than 2048 routes
+        uint32_t* pairs = (uint32_t*)routes;
+        for (int i = tid; i < kMaxExperts / 2; i += blockDim.x) pairs[i] = 0u;
         lds_barrier();
-        for (int i = tid; i < a.n; i += NW * kWave) {
-            int v = a.ids[i] - a.first;
-            if ((unsigned)v >= (unsigned)a.E || (a.mask && a.mask[i] == 0)) v = -1;
-            id[i] = (int16_t)v;
-            if (v >= 0) atomicOr(&bits[v >> 5], 1u << (v & 31));
+        for (int i = tid; i < a.n; i += blockDim.x) {
+            // in 64 bits: an id far outside may not wrap into the range
+            const long long v = (long long)a.ids[i] - a.first;
+            const bool live = v >= 0 && v < a.E && !(a.mask && a.mask[i] == 0);
+            id[i] = (int16_t)(live ? (int)v : -1);
+            if (live) atomicAdd(&pairs[v >> 1], 1u << (16 * (v & 1)));
         }
         lds_barrier();
-        const uint32_t word = lane < kMaxExperts / 32 ? bits[lane] : 0u;
-        const int pop = __popc(word);
-        const int inc = wave_inclusive_sum(pop);
-        const int total = __builtin_amdgcn_readlane(inc, kWave - 1);
-        *total_out = total;
-        if (slot >= total) return false;
-        const uint64_t hit = __ballot(slot >= inc - pop && slot < inc);
-        const int at = (int)__builtin_ctzll(hit);
-        int rem = slot - (__builtin_amdgcn_readlane(inc, at) - __builtin_amdgcn_readlane(pop, at));
-        uint32_t bw = (uint32_t)__builtin_amdgcn_readlane((int)word, at);
-        for (; rem > 0; --rem) bw &= bw - 1;
-        const int e = at * 32 + __builtin_ctz(bw);
+        if (tid < kWave) {
+            int js = 0, ss = 0;
+            for (int e0 = 0; e0 < a.E; e0 += kWave) {
+                const int e = e0 + tid;
+                const int c = e < a.E ? routes[e] : 0;
+                const int mine = (c + kCols - 1) / kCols;
+                const int inc = wave_inclusive_sum(mine);
+                for (int k = 0; k < mine; ++k) {
+                    job[js + inc - mine + k] = (uint16_t)e;
+                    pass[js + inc - mine + k] = (uint8_t)k;
+                }
+                js += __builtin_amdgcn_readlane(inc, kWave - 1);
+                ss += __popcll(__ballot(c > 0));
+            }
+            if (tid == 0) {
+                slots = ss;
+                jobs = js;
+            }
+        }
+        lds_barrier();
+        return __builtin_amdgcn_readfirstlane(jobs);
+    }
 
+    __device__ __forceinline__ int expert_of(int j, int* c0) const {
+        *c0 = __builtin_amdgcn_readfirstlane(pass[j]) * kCols;
+        return __builtin_amdgcn_readfirstlane(job[j]);
+    }
+
+    // `list` = the routes of expert e; returns their count. *off: routes of
+    // lower experts.
+    __device__ __forceinline__ int find(const RowsArgs& a, int e, int* off_out) {
+        const int lane = lane_id();
+        const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x) / kWave;
+        const int nw = blockDim.x / kWave;
         // each wave takes a range of whole 64-route rounds
         const int rounds = (a.n + kWave - 1) / kWave;
-        const int r0 = rounds * wave / NW, r1 = rounds * (wave + 1) / NW;
+        const int r0 = rounds * wave / nw, r1 = rounds * (wave + 1) / nw;
         int c = 0, l = 0;
         for (int r = r0; r < r1; ++r) {
             const int i = r * kWave + lane;
@@ -356,10 +478,9 @@ struct Finder {
             less[wave] = l;
         }
         lds_barrier();
-        int base = 0, cnt = 0, off = 0;
-        for (int w = 0; w < NW; ++w) {
+        int base = 0, off = 0;
+        for (int w = 0; w < nw; ++w) {
             if (w < wave) base += count[w];
-            cnt += count[w];
             off += less[w];
         }
         for (int r = r0; r < r1; ++r) {
@@ -370,128 +491,308 @@ struct Finder {
             base += __popcll(m);
         }
         lds_barrier();
-        *e_out = e;
-        *cnt_out = cnt;
         *off_out = off;
-        return true;
+        return __builtin_amdgcn_readfirstlane(routes[e]);
+    }
+
+    // What the layer's second kernel reads: the slots, from work-group 0, and
+    // an expert's routes, from the one that has its first rows.
+    __device__ __forceinline__ void write_slots(Table* t) const {
+        if (blockIdx.x != 0 || blockIdx.y != 0 || threadIdx.x >= kWave) return;
+        const int lane = lane_id();
+        int s0 = 0, off = 0;
+        for (int e0 = 0; e0 < kMaxExperts; e0 += kWave) {
+            const int c = routes[e0 + lane];
+            const uint64_t m = __ballot(c > 0);
+            const int inc = wave_inclusive_sum(c);
+            if (c > 0) {
+                const int s = s0 + count_below(m);
+                t->expert[s] = e0 + lane;
+                t->offset[s] = off + inc - c;
+            }
+            s0 += __popcll(m);
+            off += __builtin_amdgcn_readlane(inc, kWave - 1);
+        }
+        if (lane == 0) {
+            t->n_slots = s0;
+            t->offset[s0] = off;
+        }
+    }
+    __device__ __forceinline__ void write_routes(Table* t, int off, int cnt) const {
+        for (int i = threadIdx.x; i < cnt; i += blockDim.x) t->route[off + i] = list[i];
     }
 };
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
-// One work-group: RT 16-row tiles (LAYER: of the gate rows, and the same of
-// the up rows) of one expert, NW waves splitting the inputs, joined in wave
-// order through LDS.
-template <class W, bool LAYER, int RT, int NTB, int NW>
-__global__ __launch_bounds__(NW* kWave) void expert_rows(const RowsArgs a) {
-    constexpr int NT = LAYER ? 2 * RT : RT;
-    __shared__ Finder<NW> s_find;
-    __shared__ f32x4 s_part[NW][NT][NTB][kWave];
-    const int tid = threadIdx.x, lane = lane_id();
-    const int wave = __builtin_amdgcn_readfirstlane(tid) / kWave;
-    const int row0 = blockIdx.x * (RT * kTile);
+// Four results of a route (rows row..row+3), from the sums over all inputs.
+template <bool LAYER>
+__device__ __forceinline__ void store_rows(const RowsArgs& a, int r, int row, f32x4 v, f32x4 up) {
+    if constexpr (LAYER) {
+        if (row >= a.I) return;
+        float h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = silu(v[k]) * up[k];
+        u32x2* dst = (u32x2*)(a.h + ((size_t)r * (a.I / 8) + row / 8) * a.terms) + (row % 8) / 4;
+        for (int n = 0; n < a.terms; ++n) {
+            const u32x2 o = {bf16x2_bits(h[0], h[1]), bf16x2_bits(h[2], h[3])};
+            dst[2 * n] = o;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float t = __uint_as_float(k & 1 ? o[k / 2] & 0xffff0000u : o[k / 2] << 16);
+                // an infinite or NaN term has no rest
+                h[k] = fabsf(t) < INFINITY ? h[k] - t : 0.0f;
+            }
+        }
+    } else {
+        const size_t at = (size_t)r * a.w.N + row;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (row + k >= a.w.N) break;
+            if (a.out_f32)
+                ((float*)a.out)[at + k] = v[k];
+            else
+                ((uint16_t*)a.out)[at + k] = (uint16_t)bf16x2_bits(v[k], 0.0f);
+        }
+    }
+}
 
-    int e = 0, cnt = a.n;
-    if (a.ids) {
-        int off = 0, total = 0;
-        const bool any = s_find.find(a, blockIdx.y, &e, &cnt, &off, &total);
-        if constexpr (LAYER) {
-            if (blockIdx.x == 0) {
-                Table* t = a.table;
-                if (blockIdx.y == 0 && tid == 0) t->n_slots = total;
-                if (any) {
-                    if (tid == 0) {
-                        t->expert[blockIdx.y] = e;
-                        t->offset[blockIdx.y] = off;
-                        if ((int)blockIdx.y == total - 1) t->offset[total] = off + cnt;
+// First row of tile i of a group of NT tiles (LAYER: half of them gate rows,
+// half the up rows that belong to them).
+template <bool LAYER, int NT>
+__device__ __forceinline__ int tile_row(const RowsArgs& a, int group, int i) {
+    if constexpr (LAYER) return (i / (NT / 2)) * a.I + (group * (NT / 2) + i % (NT / 2)) * kTile;
+    return (group * NT + i) * kTile;
+}
+
+// Products for few routes an expert: a work-group's waves split the inputs,
+// XC chunks each, and hold their part of up to 8 routes' inputs in
+// registers; then only weights move. The work-groups share all (job, row
+// group) pairs equally, to one pair, and go through theirs group by group:
+// tiles are loaded NT - 1 ahead, and after a group's NT tiles the waves'
+// sums meet in LDS, where one wave (another each time) adds them up in wave
+// order and stores them while the others go on.
+template <class W, bool LAYER, int NT, int XC>
+__global__ __launch_bounds__(kMaxWaves* kWave) void expert_rows_held(const RowsArgs a,
+                                                                     int groups) {
+    static_assert(NT == 2 || NT == 4, "two tiles are joined at once");
+    __shared__ Finder s_find;
+    extern __shared__ f32x4 s_part[];  // [2][nw][NT][32]
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x) / kWave;
+    const int nw = blockDim.x / kWave;
+    const int KC = chunks<W>(a.w.K), full = a.w.KV / (W::kSteps * 8);
+    const int ck0 = wave * XC;
+    const Buffer xb = buffer_of(a.x, (uint32_t)(a.n / a.div) * a.w.KV * 16u);
+    const typename W::Lane l = W::lane_of(a.w, lane);
+    const int i16 = lane & 15, q = lane >> 4;
+    const bool wanted = (i16 < 8) == (q < 2);
+    const int part = (q >> 1) * 16 + (q & 1) * 8 + (i16 & 7);
+
+    const int total = a.ids ? s_find.begin(a) : (a.n + kCols - 1) / kCols;
+    if constexpr (LAYER) s_find.write_slots(a.table);
+    const long long items = (long long)total * groups;
+    const long long end = items * (blockIdx.x + 1) / gridDim.x;
+    int turn = 0, found = -1, cnt = a.n;
+    for (long long at = items * blockIdx.x / gridDim.x; at < end;) {
+        const int job = (int)(at / groups), g0 = (int)(at - (long long)job * groups);
+        const int g1 = (int)min((long long)groups, g0 + end - at);
+        at += g1 - g0;
+        int e = 0, c0 = job * kCols;
+        if (a.ids) {
+            e = s_find.expert_of(job, &c0);
+            if (e != found) {
+                int off;
+                lds_barrier();  // the last expert's list has been used
+                cnt = s_find.find(a, e, &off);
+                found = e;
+                if constexpr (LAYER) {
+                    if (g0 == 0 && c0 == 0) s_find.write_routes(a.table, off, cnt);
+                }
+            }
+        }
+        u32x4 x[XC][1][W::kSteps];
+        typename W::Reg r[NT][XC][1];
+        f32x4 acc[NT][1][1];
+        Input<1> xp;
+        const int jx = min(c0 + (lane & 7), cnt - 1);
+        xp.row((a.ids ? s_find.list[jx] : jx) / a.div, a.w.KV, lane);
+        any_of<XC>([&](auto j) MEP_INLINE {
+            const int c = min(ck0 + j, KC - 1);
+            xp.load(x[j][0], xb, c);
+            return false;
+        });
+        auto load = [&](int g, auto i) MEP_INLINE {
+            const typename W::Ptr p = W::at(a.w, e, tile_row<LAYER, NT>(a, g, i));
+            any_of<XC>([&](auto j) MEP_INLINE {
+                W::load(r[i][j][0], p, l, min(ck0 + j, KC - 1));
+                return false;
+            });
+        };
+        auto use = [&](auto i) MEP_INLINE {
+            acc[i][0][0] = f32x4{0, 0, 0, 0};
+            any_of<XC>([&](auto j) MEP_INLINE {
+                if (ck0 + j < KC) {
+                    if (ck0 + j == full) W::cut(r[i][j][0], l, a.w, full);
+                    W::template mma<1, 1>(r[i][j], x[j], acc[i]);
+                }
+                return false;
+            });
+        };
+        auto join = [&](int g) MEP_INLINE {
+            f32x4* buf = s_part + (turn & 1) * (nw * NT * 32);
+            if (wanted) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) buf[(wave * NT + i) * 32 + part] = acc[i][0][0];
+            }
+            lds_barrier();
+            // Lane: half of the inputs (bit 4), one of two tiles (bit 5). The
+            // next write to this buffer comes two groups later, after a
+            // barrier that this wave only reaches when it is done here.
+            if (turn % nw == wave) {
+#pragma unroll
+                for (int u = 0; u < NT / 2; ++u) {
+                    const int i = LAYER ? u + (lane >> 5) * (NT / 2) : u * 2 + (lane >> 5);
+                    f32x4 v = {0, 0, 0, 0}, o;
+                    for (int w = 0; w < nw; ++w) {
+                        const f32x4 t = buf[(w * NT + i) * 32 + (lane & 31)];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = v[k] + t[k];
                     }
-                    for (int i = tid; i < cnt; i += NW * kWave) t->route[off + i] = s_find.list[i];
-                }
-            }
-        }
-        if (!any) return;
-    }
-
-    const int KC = (a.w.K + kChunk - 1) / kChunk;
-    const int lo = KC * wave / NW, hi = KC * (wave + 1) / NW;
-    const bool live_tile = !LAYER || row0 < a.I;
-    typename W::Ptr wp[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        const int r = LAYER ? (i / RT) * a.I + row0 + (i % RT) * kTile : row0 + i * kTile;
-        wp[i] = W::at(a.w, e, r, lane);
-    }
-
-    for (int c0 = 0; c0 < cnt; c0 += NTB * 16) {
-        f32x4 acc[NT][NTB];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int b = 0; b < NTB; ++b) acc[i][b] = f32x4{0, 0, 0, 0};
-        if (live_tile) {
-            PlainInput xp[NTB];
-#pragma unroll
-            for (int b = 0; b < NTB; ++b) {
-                const int j = min(c0 + b * 16 + (lane & 15), cnt - 1);
-                const int r = a.ids ? s_find.list[j] : j;
-                xp[b].p = a.x + (size_t)(r / a.div) * a.w.KV;
-            }
-            stream<W, PlainInput, NT, NTB>(a.w, wp, xp, lo, hi, lane, acc);
-        }
-        if (c0) lds_barrier();  // the last block's sums have been read
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int b = 0; b < NTB; ++b) s_part[wave][i][b][lane] = acc[i][b];
-        lds_barrier();
-        for (int u = wave; u < RT * NTB; u += NW) {
-            const int i = u / NTB, b = u % NTB;
-            const int j = c0 + b * 16 + (lane & 15);
-            if (j >= cnt) continue;
-            const int r = a.ids ? s_find.list[j] : j;
-            const int row = row0 + i * kTile + (lane >> 4) * 4;
-            f32x4 v = s_part[0][i][b][lane];
-#pragma unroll
-            for (int w = 1; w < NW; ++w) {
-                const f32x4 o = s_part[w][i][b][lane];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = v[k] + o[k];
-            }
-            if constexpr (LAYER) {
-                f32x4 up = s_part[0][RT + i][b][lane];
-#pragma unroll
-                for (int w = 1; w < NW; ++w) {
-                    const f32x4 o = s_part[w][RT + i][b][lane];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) up[k] = up[k] + o[k];
-                }
-                float h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h[k] = row + k < a.I ? silu(v[k]) * up[k] : 0.0f;
-                u32x2* dst = (u32x2*)(a.h + ((size_t)r * (a.Ip / 8) + row / 8) * a.terms) +
-                             (row % 8) / 4;
-                for (int n = 0; n < a.terms; ++n) {
-                    const u32x2 o = {bf16x2_bits(h[0], h[1]), bf16x2_bits(h[2], h[3])};
-                    dst[2 * n] = o;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float b =
-                            __uint_as_float(k & 1 ? o[k / 2] & 0xffff0000u : o[k / 2] << 16);
-                        // an infinite or NaN term has no rest
-                        h[k] = fabsf(b) < INFINITY ? h[k] - b : 0.0f;
+                        v[k] = v[k] + __shfl(v[k], lane ^ 16, kWave);
+                        o[k] = LAYER ? __shfl(v[k], lane ^ 32, kWave) : 0.0f;
                     }
-                }
-            } else {
-                const size_t at = (size_t)r * a.w.N + row;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (row + k >= a.w.N) break;
-                    if (a.out_f32)
-                        ((float*)a.out)[at + k] = v[k];
-                    else
-                        ((uint16_t*)a.out)[at + k] = (uint16_t)bf16x2_bits(v[k], 0.0f);
+                    const int j = c0 + (lane & 7);
+                    const int row =
+                        tile_row<LAYER, NT>(a, g, LAYER ? u : i) + ((lane >> 3) & 1) * 4;
+                    if ((lane & 16) == 0 && (!LAYER || lane < 32) && j < cnt)
+                        store_rows<LAYER>(a, a.ids ? s_find.list[j] : j, row, v, o);
                 }
             }
+            ++turn;
+        };
+        any_of<NT - 1>([&](auto i) MEP_INLINE {
+            load(g0, i);
+            return false;
+        });
+        any_of<XC>([&](auto j) MEP_INLINE {
+            if (ck0 + j >= full) Input<1>::cut(x[j][0], ck0 + j, a.w.KV, lane);
+            return false;
+        });
+        for (int g = g0; g + 1 < g1; ++g) {
+            any_of<NT>([&](auto i) MEP_INLINE {
+                load(i == 0 ? g : g + 1, std::integral_constant<int, (i + NT - 1) % NT>{});
+                use(i);
+                return false;
+            });
+            join(g);
+        }
+        load(g1 - 1, std::integral_constant<int, NT - 1>{});
+        any_of<NT>([&](auto i) MEP_INLINE {
+            use(i);
+            return false;
+        });
+        join(g1 - 1);
+    }
+}
+
+// Products for more routes an expert: one work-group has RT tiles (LAYER: of
+// the gate rows, and the same of the up rows) of one slot, NW waves
+// splitting the inputs, and reads the inputs along with the weights, for up
+// to 16 routes at a time.
+template <class W, bool LAYER, int RT, int NB, int NW>
+__device__ __forceinline__ void rows_pass(const RowsArgs& a, const Finder& find, f32x4* s_part,
+                                          int e, int cnt, int c0, int row0, Buffer xb) {
+    constexpr int NT = LAYER ? 2 * RT : RT;
+    const int lane = lane_id();
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x) / kWave;
+    const int KC = chunks<W>(a.w.K);
+    const int i16 = lane & 15, q = lane >> 4;
+    typename W::Ptr wp[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) wp[i] = W::at(a.w, e, (i / RT) * a.I + row0 + (i % RT) * kTile);
+    f32x4 acc[NT][NB];
+    Input<1> xp[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int j = min(c0 + b * kCols + (lane & 7), cnt - 1);
+        xp[b].row((a.ids ? find.list[j] : j) / a.div, a.w.KV, lane);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) acc[i][b] = f32x4{0, 0, 0, 0};
+    }
+    stream<W, 2, 1, NT, NB>(a.w, wp, xb, xp, KC * wave / NW, KC * (wave + 1) / NW, lane, acc);
+    if (c0) lds_barrier();  // the last pass's sums have been read
+    // [wave][tile][block][32]
+    if ((i16 < 8) == (q < 2)) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                s_part[((wave * NT + i) * NB + b) * 32 + (q >> 1) * 16 + (q & 1) * 8 + (i16 & 7)] =
+                    acc[i][b];
+    }
+    lds_barrier();
+    // 16 threads per (tile, block): 8 routes x 2 row quads
+    for (int u = threadIdx.x; u < RT * NB * 16; u += NW * kWave) {
+        const int i = u / (NB * 16), b = (u / 16) % NB, s = u & 15;
+        const int j = c0 + b * kCols + (s & 7);
+        if (j >= cnt) continue;
+        f32x4 v = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x4 o = s_part[((w * NT + i) * NB + b) * 32 + h * 16 + s];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = v[k] + o[k];
+                if constexpr (LAYER) {
+                    const f32x4 t = s_part[((w * NT + RT + i) * NB + b) * 32 + h * 16 + s];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) up[k] = up[k] + t[k];
+                }
+            }
+        store_rows<LAYER>(a, a.ids ? find.list[j] : j, row0 + i * kTile + (s >> 3) * 4, v, up);
+    }
+}
+
+template <class W, bool LAYER, int RT, int NW>
+__global__ __launch_bounds__(NW* kWave, RD_WPE) void expert_rows_read(const RowsArgs a) {
+    __shared__ Finder s_find;
+    __shared__ f32x4 s_part[NW * (LAYER ? 2 : 1) * RT * 2 * 32];
+    const int row0 = blockIdx.x * (RT * kTile);
+    int e = 0, cnt = a.n;
+    if (a.ids) {
+        s_find.begin(a);
+        if constexpr (LAYER) s_find.write_slots(a.table);
+        // the blockIdx.y-th slot
+        int slot = blockIdx.y;
+        if (slot >= s_find.slots) return;
+        for (int e0 = 0;; e0 += kWave) {
+            const uint64_t m = __ballot(s_find.routes[e0 + lane_id()] > 0);
+            const int here = __popcll(m);
+            if (slot < here) {
+                const bool hit = ((m >> lane_id()) & 1) && count_below(m) == slot;
+                e = e0 + (int)__builtin_ctzll(__ballot(hit));
+                break;
+            }
+            slot -= here;
+        }
+        int off;
+        cnt = s_find.find(a, e, &off);
+        if constexpr (LAYER) {
+            if (blockIdx.x == 0) s_find.write_routes(a.table, off, cnt);
+        }
+    }
+    const Buffer xb = buffer_of(a.x, (uint32_t)(a.n / a.div) * a.w.KV * 16u);
+    for (int c0 = 0; c0 < cnt;) {
+        if (cnt - c0 > kCols) {
+            rows_pass<W, LAYER, RT, 2, NW>(a, s_find, s_part, e, cnt, c0, row0, xb);
+            c0 += 2 * kCols;
+        } else {
+            rows_pass<W, LAYER, RT, 1, NW>(a, s_find, s_part, e, cnt, c0, row0, xb);
+            c0 += kCols;
         }
     }
 }
@@ -500,7 +801,6 @@ __global__ __launch_bounds__(NW* kWave) void expert_rows(const RowsArgs a) {
 
 struct DownArgs {
     const u32x4* h;
-    int Ip;
     const Table* table;
     const float* scores;  // [T*K]
     int T, K, n, E;
@@ -509,87 +809,181 @@ struct DownArgs {
     float* out_f32;
 };
 
-// One work-group: RT 16-row tiles of the output for all tokens, its waves
-// splitting the (expert, chunk) steps of all experts reached. A wave adds
-// score * product into its own [token][row] sums in LDS after each expert it
+// A job: up to two column blocks of one expert's routes.
+struct Job {
+    uint16_t expert, cnt;
+    int off;
+};
+
+// One work-group: RT 8-row tiles of the output for all tokens, its waves
+// splitting the (job, chunk) steps of all experts reached in equal, unbroken
+// ranges; a step's loads are issued one step ahead, across jobs. A wave adds
+// score * product into its own [token][row] sums in LDS after each job it
 // visits; the waves' sums are joined in wave order at the end. Every sum has
 // a fixed order, so equal inputs give equal bits.
-template <class W, int TERMS, int RT, int NTB, int NW>
-__global__ __launch_bounds__(NW* kWave) void expert_down(const DownArgs a) {
+template <class W, int TERMS, int RT, int NW>
+__global__ __launch_bounds__(NW* kWave, DN_WPE) void expert_down(const DownArgs a) {
     extern __shared__ f32x4 s_dyn[];
-    constexpr int R4 = RT * 4;  // row quads
+    __shared__ int s_jobs;
+    constexpr int R4 = RT * 2;  // row quads
+    constexpr int kRoutes = Input<TERMS>::kRoutes;
     const int tid = threadIdx.x, lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(tid) / kWave;
-    const int slots_max = min(a.n, a.E);
-    f32x4* s_sum = s_dyn;                                   // [NW][T][R4]
-    float* s_score = (float*)(s_dyn + NW * a.T * R4);       // [n]
-    int* s_expert = (int*)(s_score + a.n);                  // [slots_max]
-    int* s_off = s_expert + slots_max;                      // [slots_max + 1]
-    uint16_t* s_route = (uint16_t*)(s_off + slots_max + 1); // [n]
+    f32x4* s_sum = s_dyn;                              // [NW][T][R4]
+    Job* s_job = (Job*)(s_dyn + NW * a.T * R4);        // [n]
+    float* s_score = (float*)(s_job + a.n);            // [n] by place in the list
+    uint16_t* s_route = (uint16_t*)(s_score + a.n);    // [n]
+    uint8_t* s_token = (uint8_t*)(s_route + a.n);      // [n]
     const int row0 = blockIdx.x * (RT * kTile);
 
     for (int i = tid; i < NW * a.T * R4; i += NW * kWave) s_sum[i] = f32x4{0, 0, 0, 0};
-    for (int i = tid; i < a.n; i += NW * kWave) {
-        s_score[i] = a.scores[i];
-        s_route[i] = a.table->route[i];
-    }
-    for (int i = tid; i < slots_max; i += NW * kWave) s_expert[i] = a.table->expert[i];
-    for (int i = tid; i < slots_max + 1; i += NW * kWave) s_off[i] = a.table->offset[i];
     const int n_slots = a.table->n_slots;
+    const int live = n_slots ? a.table->offset[n_slots] : 0;
+    for (int i = tid; i < live; i += NW * kWave) {
+        const int r = a.table->route[i];
+        s_route[i] = (uint16_t)r;
+        s_score[i] = a.scores[r];
+        s_token[i] = (uint8_t)(r / a.K);
+    }
+    if (wave == 0) {
+        int jobs = 0;
+        for (int s0 = 0; s0 < n_slots; s0 += kWave) {
+            const int s = s0 + lane;
+            const bool in = s < n_slots;
+            const int e = in ? a.table->expert[s] : 0;
+            const int off = in ? a.table->offset[s] : 0;
+            const int cnt = in ? a.table->offset[s + 1] - off : 0;
+            const int mine = (cnt + 2 * kRoutes - 1) / (2 * kRoutes);
+            const int inc = wave_inclusive_sum(mine);
+            for (int j = 0; j < mine; ++j)
+                s_job[jobs + inc - mine + j] = {(uint16_t)e,
+                                                (uint16_t)min(2 * kRoutes, cnt - j * 2 * kRoutes),
+                                                off + j * 2 * kRoutes};
+            jobs += __builtin_amdgcn_readlane(inc, kWave - 1);
+        }
+        if (lane == 0) s_jobs = jobs;
+    }
     lds_barrier();
 
-    const int KC = (a.w.K + kChunk - 1) / kChunk;
-    const int steps = n_slots * KC;
-    const int lo = (int)((long long)steps * wave / NW), hi = (int)((long long)steps * (wave + 1) / NW);
+    const int KC = chunks<W>(a.w.K), full = a.w.KV / (W::kSteps * 8);
+    const long long steps = (long long)s_jobs * KC;
+    const int lo = (int)(steps * wave / NW), hi = (int)(steps * (wave + 1) / NW);
     f32x4* sum = s_sum + (size_t)wave * a.T * R4;
-    for (int at = lo; at < hi;) {
-        const int slot = at / KC;
-        const int k0 = at - slot * KC, k1 = min(KC, k0 + hi - at);
-        at += k1 - k0;
-        const int e = __builtin_amdgcn_readfirstlane(s_expert[slot]);
-        const int off = __builtin_amdgcn_readfirstlane(s_off[slot]);
-        const int cnt = __builtin_amdgcn_readfirstlane(s_off[slot + 1]) - off;
+    const Buffer hb = buffer_of(a.h, (uint32_t)a.n * a.w.KV * (TERMS * 16u));
+    const typename W::Lane l = W::lane_of(a.w, lane);
+
+    if (lo < hi) {
+        typename W::Reg r[2][RT];
+        u32x4 x[2][2][W::kSteps];
+        f32x4 acc[RT][2];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+        struct At {
+            int job, chunk, blocks;
+        };
         typename W::Ptr wp[RT];
+        Input<TERMS> xp[2];
+        auto open = [&](At& p) MEP_INLINE {  // points the loads at a job
+            const Job j = s_job[p.job];
+            const int e = __builtin_amdgcn_readfirstlane(j.expert);
+            const int cnt = __builtin_amdgcn_readfirstlane(j.cnt);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) wp[i] = W::at(a.w, e, row0 + i * kTile, lane);
-        for (int c0 = 0; c0 < cnt; c0 += NTB * 16) {
-            f32x4 acc[RT][NTB];
-            SplitInput<TERMS> xp[NTB];
-            int tok[NTB];
-            float sc[NTB];
+            for (int i = 0; i < RT; ++i) wp[i] = W::at(a.w, e, row0 + i * kTile);
 #pragma unroll
-            for (int b = 0; b < NTB; ++b) {
-                const int j = c0 + b * 16 + (lane & 15);
-                const int r = s_route[off + min(j, cnt - 1)];
-                xp[b].p = a.h + (size_t)r * (a.Ip / 8) * TERMS;
-                tok[b] = j < cnt ? r / a.K : -1;
-                sc[b] = s_score[r];
+            for (int b = 0; b < 2; ++b)
+                xp[b].row(s_route[j.off + min(b * kRoutes + (lane & (kRoutes - 1)), cnt - 1)],
+                          a.w.KV, lane);
+            p.blocks = cnt > kRoutes ? 2 : 1;
+        };
+        auto load = [&](int d, const At& p) MEP_INLINE {
+            xp[0].load(x[d][0], hb, p.chunk);
 #pragma unroll
-                for (int i = 0; i < RT; ++i) acc[i][b] = f32x4{0, 0, 0, 0};
+            for (int i = 0; i < RT; ++i) W::load(r[d][i], wp[i], l, p.chunk);
+            if (p.blocks == 2) xp[1].load(x[d][1], hb, p.chunk);
+        };
+        auto next = [&](At& p) MEP_INLINE {
+            if (++p.chunk == KC) {
+                p.chunk = 0;
+                ++p.job;
+                open(p);
             }
-            stream<W, SplitInput<TERMS>, RT, NTB>(a.w, wp, xp, k0, k1, lane, acc);
+        };
+        auto fold = [&](int job) MEP_INLINE {  // adds the sums of a job's routes to their tokens'
+            const Job j = s_job[job];
+            const int cnt = __builtin_amdgcn_readfirstlane(j.cnt);
+            const int blocks = cnt > kRoutes ? 2 : 1;
+            for (int b = 0; b < blocks; ++b) {
+                const int c = b * kRoutes + (lane & (kRoutes - 1));
+                bool todo = lane < 32 && (lane & 15) < kRoutes && c < cnt;
+                const int tok = s_token[j.off + min(c, cnt - 1)];
+                const float sc = s_score[j.off + min(c, cnt - 1)];
+                f32x4 v[RT];
 #pragma unroll
-            for (int b = 0; b < NTB; ++b) {
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[i][k] = Input<TERMS>::total(b ? acc[i][1][k] : acc[i][0][k], lane);
                 // a token that names an expert twice has adjacent columns:
                 // they are added one after the other
-                bool todo = tok[b] >= 0;
                 while (__ballot(todo)) {
-                    const int before = __shfl(todo ? tok[b] : -1, max(lane - 1, 0), kWave);
-                    const bool now = todo && ((lane & 15) == 0 || before != tok[b]);
-                    if (now) {
+                    const int before = __shfl(todo ? tok : -1, max(lane - 1, 0), kWave);
+                    if (todo && ((lane & 15) == 0 || before != tok)) {
 #pragma unroll
                         for (int i = 0; i < RT; ++i) {
-                            f32x4* s = sum + tok[b] * R4 + i * 4 + (lane >> 4);
-                            f32x4 v = *s;
+                            f32x4* s = sum + tok * R4 + i * 2 + (lane >> 4);
+                            f32x4 o = *s;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                v[k] = __builtin_fmaf(sc[b], acc[i][b][k], v[k]);
-                            *s = v;
+                            for (int k = 0; k < 4; ++k) o[k] = __builtin_fmaf(sc, v[i][k], o[k]);
+                            *s = o;
                         }
                         todo = false;
                     }
                 }
             }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
+        };
+        auto use = [&](int d, const At& p, bool last) MEP_INLINE {
+            if (p.chunk == full) {
+#pragma unroll
+                for (int i = 0; i < RT; ++i) W::cut(r[d][i], l, a.w, full);
+                Input<TERMS>::cut(x[d][0], full, a.w.KV, lane);
+                Input<TERMS>::cut(x[d][1], full, a.w.KV, lane);
+            }
+            if (p.blocks == 2) {
+                W::template mma<RT, 2>(r[d], x[d], acc);
+            } else {
+                u32x4(&x1)[1][W::kSteps] = reinterpret_cast<u32x4(&)[1][W::kSteps]>(x[d][0]);
+                f32x4 one[RT][1];
+#pragma unroll
+                for (int i = 0; i < RT; ++i) one[i][0] = acc[i][0];
+                W::template mma<RT, 1>(r[d], x1, one);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) acc[i][0] = one[i][0];
+            }
+            if (last || p.chunk == KC - 1) fold(p.job);
+        };
+        At p[2];
+        p[0] = {lo / KC, lo % KC, 1};
+        open(p[0]);
+        load(0, p[0]);
+        for (int s = lo;; ++s) {
+            if (s + 1 >= hi) {
+                use(0, p[0], true);
+                break;
+            }
+            p[1] = p[0];
+            next(p[1]);
+            load(1, p[1]);
+            use(0, p[0], false);
+            if (++s + 1 >= hi) {
+                use(1, p[1], true);
+                break;
+            }
+            p[0] = p[1];
+            next(p[0]);
+            load(0, p[0]);
+            use(1, p[1], false);
         }
     }
     lds_barrier();
@@ -612,37 +1006,74 @@ __global__ __launch_bounds__(NW* kWave) void expert_down(const DownArgs a) {
 
 // ----------------------------------------------------------------- launch
 
-inline size_t down_lds(int nw, int rt, int T, int n, int E) {
-    const int slots = n < E ? n : E;
-    return (size_t)nw * T * rt * 4 * 16 + (size_t)n * 6 + (size_t)(2 * slots + 1) * 4 + 8;
+constexpr int kCus = 256;
+
+inline int tiles_of(int rows, int rt) { return (rows + rt * kTile - 1) / (rt * kTile); }
+
+#ifndef HELD_MIN
+#define HELD_MIN 2048
+#endif
+#ifndef HELD_NT1
+#define HELD_NT1 4
+#define HELD_NT2 2
+#endif
+#ifndef READ_RT
+#define READ_RT 2
+#define READ_NW 4
+#endif
+#ifndef DN_RT
+#define DN_RT 2
+#define DN_NW 4
+#endif
+
+template <class W, bool LAYER, int NT, int XC>
+void launch_held(hipStream_t s, const RowsArgs& a, int kc) {
+    const int nw = (kc + XC - 1) / XC;
+    const int groups = tiles_of(LAYER ? a.I : a.w.N, LAYER ? NT / 2 : NT);
+    const int slots = a.ids ? (a.n < a.E ? a.n : a.E) : 1;
+    const long long items = (long long)slots * groups;
+    const long long wgs = (long long)kCus * (kMaxWaves / nw);
+    hipLaunchKernelGGL((expert_rows_held<W, LAYER, NT, XC>), dim3(items < wgs ? items : wgs),
+                       dim3(nw * kWave), (size_t)2 * nw * NT * 32 * 16, s, a, groups);
 }
 
-template <class W>
-void launch_matvec(hipStream_t s, const RowsArgs& a) {
-    constexpr int NW = 8, RT = 1;
+template <class W, bool LAYER>
+void launch_rows(hipStream_t s, const RowsArgs& a) {
+    const int kc = chunks<W>(a.w.K);
     const int slots = a.ids ? (a.n < a.E ? a.n : a.E) : 1;
-    const dim3 g((a.w.N + RT * kTile - 1) / (RT * kTile), slots), b(NW * kWave);
-    hipLaunchKernelGGL((expert_rows<W, false, RT, 1, NW>), g, b, 0, s, a);
+    const int rows = LAYER ? a.I : a.w.N;
+    if (a.n <= kCols * slots && kc <= W::kMaxHeld * kMaxWaves && (long long)slots * tiles_of(rows, 1) >= HELD_MIN) {
+        if (kc <= kMaxWaves)
+            launch_held<W, LAYER, HELD_NT1, 1>(s, a, kc);
+        else if (kc <= 2 * kMaxWaves)
+            launch_held<W, LAYER, HELD_NT2, 2>(s, a, kc);
+        else if constexpr (W::kMaxHeld == 4)
+            launch_held<W, LAYER, 2, 4>(s, a, kc);
+        return;
+    }
+    constexpr int RT = READ_RT, NW = READ_NW;
+    hipLaunchKernelGGL((expert_rows_read<W, LAYER, RT, NW>), dim3(tiles_of(rows, RT), slots),
+                       dim3(NW * kWave), 0, s, a);
+}
+
+inline size_t down_lds(int nw, int rt, int T, int n) {
+    return (size_t)nw * T * rt * 2 * 16 + (size_t)n * (8 + 4 + 2 + 1) + 16;
 }
 
 template <class W, int TERMS>
 void launch_down(hipStream_t s, const DownArgs& d) {
-    constexpr int RT = 1;
-    const dim3 g((d.w.N + RT * kTile - 1) / (RT * kTile));
-    if (d.T <= 64)
-        hipLaunchKernelGGL((expert_down<W, TERMS, RT, 1, 8>), g, dim3(8 * kWave),
-                           down_lds(8, RT, d.T, d.n, d.E), s, d);
-    else
-        hipLaunchKernelGGL((expert_down<W, TERMS, RT, 1, 4>), g, dim3(4 * kWave),
-                           down_lds(4, RT, d.T, d.n, d.E), s, d);
+    hipLaunchKernelGGL((expert_down<W, TERMS, DN_RT, DN_NW>), dim3(tiles_of(d.w.N, DN_RT)),
+                       dim3(DN_NW * kWave), down_lds(DN_NW, DN_RT, d.T, d.n), s, d);
+}
+
+template <class W>
+void launch_matvec(hipStream_t s, const RowsArgs& a) {
+    launch_rows<W, false>(s, a);
 }
 
 template <class W>
 void launch_layer(hipStream_t s, const RowsArgs& a, const DownArgs& d) {
-    constexpr int RT = 1;
-    const int slots = a.n < a.E ? a.n : a.E;
-    const dim3 g(a.Ip / (RT * kTile), slots), b(8 * kWave);
-    hipLaunchKernelGGL((expert_rows<W, true, RT, 1, 8>), g, b, 0, s, a);
+    launch_rows<W, true>(s, a);
     if (a.terms == 2)
         launch_down<W, 2>(s, d);
     else

@@ -37,16 +37,13 @@ int view_of(const mep_weights* m, Weights* w) {
     w->K = m->K;
     w->KV = m->K / 8;
     w->tiles = (m->N + kTile - 1) / kTile;
-    w->KB = (m->K + kChunk - 1) / kChunk;
-    w->KS = (m->K + 511) / 512;
+    w->KB = (m->K + kPackK - 1) / kPackK;
     return MEP_OK;
 }
 
 Kind kind_of(const mep_weights* m) {
     return {m->group, m->zeros != nullptr, m->scale_dtype == MEP_SCALE_F16};
 }
-
-int padded_inner(int I) { return (I + kChunk - 1) / kChunk * kChunk; }
 
 size_t table_bytes() { return (sizeof(Table) + 255) / 256 * 256; }
 
@@ -91,7 +88,7 @@ extern "C" size_t mep_moe_layer_workspace_size(int T, int K, int I) {
     if (T < 0 || T > kMaxLayerTokens || K < 1 || (long long)T * K > kMaxRoutes || I < 8 ||
         I > kMaxDim || I % 8 != 0)
         return 0;
-    return table_bytes() + (size_t)T * K * padded_inner(I) * 2 * 3;  // up to 3 terms
+    return table_bytes() + (size_t)T * K * I * 2 * 3;  // up to 3 bf16 terms
 }
 
 extern "C" int mep_moe_layer(int T, int K, int H, int I, int first, const uint16_t* x,
@@ -126,12 +123,10 @@ extern "C" int mep_moe_layer(int T, int K, int H, int I, int first, const uint16
     a.w = up;
     a.h = (u32x4*)((char*)workspace + table_bytes());
     a.I = I;
-    a.Ip = padded_inner(I);
     a.terms = out_f32 ? 3 : 2;
     a.table = (Table*)workspace;
     DownArgs d = {};
     d.h = a.h;
-    d.Ip = a.Ip;
     d.table = a.table;
     d.scores = scores;
     d.T = T;

@@ -11,9 +11,9 @@ using namespace experts;
 
 constexpr int kPackThreads = 256;
 
-// One thread: the 32 codes that one lane of the product kernel loads at once
-// for one 16-row tile and 128 inputs: row lane % 16, and for each of the
-// chunk's four MFMAs j the 8 inputs 32 j + 8 (lane / 16) .. + 7 as one word.
+// One thread: the 32 codes that one lane of the product kernels loads at
+// once for one 8-row tile and 256 inputs: row lane % 8, and for each of the
+// block's four 64-input steps j the 8 inputs of vector lane_vec as one word.
 // In a word, int4 code m lies at bit 4 (m / 2) of half m % 2, so that a
 // shift and a mask leave two neighbours in the halves; 4-bit floats lie in
 // order, as the conversion instruction takes them. Rows past N and inputs
@@ -28,14 +28,14 @@ __global__ __launch_bounds__(kPackThreads) void pack_codes(const uint8_t* __rest
     const size_t blk = at >> 6;
     const int kb = (int)(blk % KB);
     const size_t et = blk / KB;
-    const int row = (int)(et % tiles) * kTile + (lane & 15);
+    const int row = (int)(et % tiles) * kTile + (lane & 7);
     const size_t e = et / tiles;
     u32x4 o = {0, 0, 0, 0};
     if (row < N) {
         const uint8_t* src = codes + (e * N + row) * (size_t)K;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int k = kb * kChunk + j * 32 + (lane >> 4) * 8;
+            const int k = kb * kPackK + j * kStep + lane_vec(lane) * 8;
             uint32_t w = 0;
             for (int m = 0; m < 8; ++m) {
                 const uint32_t q = k + m < K ? src[k + m] & 15u : 0u;
@@ -47,27 +47,29 @@ __global__ __launch_bounds__(kPackThreads) void pack_codes(const uint8_t* __rest
     out[at] = o;
 }
 
-// [E,N,G] -> [E][tile][superblock][4 row quads][512 / group][4 rows]; places
-// past N or the last group hold zero.
+// [E,N,G] -> [E][tile][block][2 row quads][groups of the block][4 rows];
+// groups of 32 with even indices come first. Places past N or the last group
+// hold zero.
 template <typename T>
 __global__ __launch_bounds__(kPackThreads) void pack_groups(const T* __restrict__ src,
                                                             T* __restrict__ out, int N, int G,
-                                                            int tiles, int KS, int per,
+                                                            int tiles, int KB, int per,
                                                             size_t total) {
     const size_t at = (size_t)blockIdx.x * kPackThreads + threadIdx.x;
     if (at >= total) return;
     size_t r = at;
     const int i = (int)(r & 3);
     r >>= 2;
-    const int gi = (int)(r % per);
+    int gi = (int)(r % per);
     r /= per;
-    const int quad = (int)(r & 3);
-    r >>= 2;
-    const int ks = (int)(r % KS);
-    r /= KS;
+    const int quad = (int)(r & 1);
+    r >>= 1;
+    const int kb = (int)(r % KB);
+    r /= KB;
     const int row = (int)(r % tiles) * kTile + quad * 4 + i;
     const size_t e = r / tiles;
-    const int g = ks * per + gi;
+    if (per == kPackK / 32) gi = (gi & 3) * 2 + (gi >> 2);
+    const int g = kb * per + gi;
     out[at] = row < N && g < G ? src[(e * N + row) * (size_t)G + g] : (T)0;
 }
 
@@ -131,7 +133,9 @@ bool sizes_ok(int E, int N, int K) {
 
 bool group_ok(int g) { return g == 32 || g == 64 || g == 128; }
 
-size_t tiles_of(int N) { return ((size_t)N + kTile - 1) / kTile; }
+size_t row_tiles(int N) { return ((size_t)N + kTile - 1) / kTile; }
+
+size_t blocks_of(int K) { return ((size_t)K + kPackK - 1) / kPackK; }
 
 dim3 blocks(size_t n, int per) { return dim3((unsigned)((n + per - 1) / per)); }
 
@@ -143,12 +147,12 @@ using namespace mep::experts;
 
 extern "C" size_t mep_packed_code_bytes(int E, int N, int K) {
     if (!sizes_ok(E, N, K)) return 0;
-    return (size_t)E * tiles_of(N) * ((K + kChunk - 1) / kChunk) * 1024;
+    return (size_t)E * row_tiles(N) * blocks_of(K) * 1024;
 }
 
 extern "C" size_t mep_packed_scale_count(int E, int N, int K, int group) {
     if (!sizes_ok(E, N, K) || !group_ok(group)) return 0;
-    return (size_t)E * tiles_of(N) * ((K + 511) / 512) * 16 * (512 / group);
+    return (size_t)E * row_tiles(N) * blocks_of(K) * 8 * (kPackK / group);
 }
 
 extern "C" int mep_pack_weights(int E, int N, int K, int kind, int group, const uint8_t* codes,
@@ -163,17 +167,17 @@ extern "C" int mep_pack_weights(int E, int N, int K, int kind, int group, const 
         (packed_zeros && !rows::aligned16(packed_zeros)) || ((uintptr_t)scales & 1u))
         return MEP_ERR_SHAPE;
     hipStream_t s = (hipStream_t)stream;
-    const int tiles = (int)tiles_of(N), KB = (K + kChunk - 1) / kChunk, KS = (K + 511) / 512;
-    const int G = (K + group - 1) / group, per = 512 / group;
+    const int tiles = (int)row_tiles(N), KB = (int)blocks_of(K);
+    const int G = (K + group - 1) / group, per = kPackK / group;
     const size_t nc = (size_t)E * tiles * KB * 64;
     const size_t ns = mep_packed_scale_count(E, N, K, group);
     hipLaunchKernelGGL(pack_codes, blocks(nc, kPackThreads), dim3(kPackThreads), 0, s, codes,
                        (u32x4*)packed_codes, N, K, tiles, KB, kind == MEP_WEIGHT_FP4 ? 1 : 0, nc);
     hipLaunchKernelGGL(pack_groups<uint16_t>, blocks(ns, kPackThreads), dim3(kPackThreads), 0, s,
-                       (const uint16_t*)scales, (uint16_t*)packed_scales, N, G, tiles, KS, per, ns);
+                       (const uint16_t*)scales, (uint16_t*)packed_scales, N, G, tiles, KB, per, ns);
     if (zeros)
         hipLaunchKernelGGL(pack_groups<uint8_t>, blocks(ns, kPackThreads), dim3(kPackThreads), 0,
-                           s, zeros, packed_zeros, N, G, tiles, KS, per, ns);
+                           s, zeros, packed_zeros, N, G, tiles, KB, per, ns);
     MEP_LAUNCH_CHECK();
     return MEP_OK;
 }

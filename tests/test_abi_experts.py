@@ -61,8 +61,9 @@ def _w(B, kind=1, E=2, N=16, K=128, group=32, sd=1, data=P, scales=P, zeros=None
 
 
 def test_packed_sizes(B):
-    assert B.mep_packed_code_bytes(2, 17, 136) == 2 * 2 * 2 * 1024
-    assert B.mep_packed_scale_count(2, 17, 520, 64) == 2 * 2 * 2 * 16 * 8
+    # 3 tiles of 8 rows; 1 and 3 blocks of 256 inputs
+    assert B.mep_packed_code_bytes(2, 17, 136) == 2 * 3 * 1 * 1024
+    assert B.mep_packed_scale_count(2, 17, 520, 64) == 2 * 3 * 3 * 8 * 4
     for a in ((0, 16, 128), (1025, 16, 128), (1, 0, 128), (1, 16, 12), (1, 16, 65544),
               (1, (1 << 20) + 1, 128)):
         assert B.mep_packed_code_bytes(*a) == 0 and B.mep_packed_scale_count(*a, 32) == 0
@@ -128,7 +129,7 @@ def test_moe_layer_validation(B):
     for kw in (dict(x=None), dict(ids=None), dict(sc=None), dict(ws=None), dict(ob=None)):
         assert _layer(B, **kw) == B.MEP_ERR_NULLPTR
     need = B.mep_moe_layer_workspace_size(4, 2, 64)
-    assert need > 8 * 128 * 4
+    assert need > 8 * 64 * 6
     for kw in (dict(wsb=need - 1), dict(ws=P + 16), dict(w13=_w(B, E=3, N=128, K=128)),
                dict(w13=_w(B, kind=2, N=128, K=128)), dict(w13=_w(B, group=64, N=128, K=128)),
                dict(w13=_w(B, sd=2, N=128, K=128)), dict(w2=_w(B, N=128, K=64, zeros=P))):
