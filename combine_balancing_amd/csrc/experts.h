@@ -55,12 +55,6 @@ constexpr int kMaxRoutes = 2048;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxLayerTokens = 128;
 constexpr int kMaxWaves = 16;
-#ifndef DN_WPE
-#define DN_WPE 1
-#endif
-#ifndef RD_WPE
-#define RD_WPE 1
-#endif
 
 // Routed list that the layer's first kernel leaves for its second.
 struct Table {
@@ -91,6 +85,7 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 // caches (weights are used once).
 typedef __amdgpu_buffer_rsrc_t Buffer;
 constexpr int kNt = 2;
+constexpr uint32_t kPast = 0x80000000u;  // an offset past every buffer's end
 
 __device__ __forceinline__ Buffer buffer_of(const void* p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00027000);
@@ -117,7 +112,9 @@ __device__ __forceinline__ int lane_vec(int lane) { return (lane >> 4) + ((lane 
 
 struct Bf16Weights {
     static constexpr int kSteps = 2;
-    static constexpr int kMaxHeld = 4;  // chunks of inputs that a wave can hold
+    static constexpr int kMaxHeld = 4;    // chunks of inputs that a wave can hold
+    static constexpr int kReadWaves = 4;  // waves per SIMD that expert_rows_read is built for
+    static constexpr bool kWide = true;   // whether expert_down takes four tiles at a time
     struct Reg {
         u32x4 a[kSteps];
     };
@@ -125,36 +122,36 @@ struct Bf16Weights {
         Buffer rows;
     };
     struct Lane {
-        uint32_t vec, bytes;
+        int left;  // vectors of the row from the lane's first on
+        uint32_t bytes;
     };
     static __device__ __forceinline__ Lane lane_of(const Weights& w, int lane) {
-        const uint32_t v = lane_vec(lane);
-        return {v, (uint32_t)((lane & 7) * w.KV + v) * 16u};
+        const int v = lane_vec(lane);
+        return {w.KV - v, (uint32_t)((lane & 7) * w.KV + v) * 16u};
     }
     static __device__ __forceinline__ Ptr at(const Weights& w, int e, int row0) {
         const u32x4* p = w.codes + ((size_t)e * w.N + min(row0, w.N - kTile)) * w.KV;
         return {buffer_of(p, (uint32_t)(kTile * w.KV) * 16u)};
     }
+    // In the chunk that K cuts, a lane's vectors past K lie in the next row:
+    // they are loaded from past the buffer, as zeros.
     static __device__ __forceinline__ void load(Reg& r, const Ptr& p, const Lane& l, int c) {
 #pragma unroll
         for (int j = 0; j < kSteps; ++j)
-            r.a[j] = buffer_load<u32x4, kNt>(p.rows, l.bytes + j * 128, c * (kSteps * 128));
+            r.a[j] = buffer_load<u32x4, kNt>(
+                p.rows, (c * kSteps + j) * 8 < l.left ? l.bytes + j * 128 : kPast,
+                c * (kSteps * 128));
     }
-    // The chunk that K cuts: a lane's vectors past it hold the next row.
-    static __device__ __forceinline__ void cut(Reg& r, const Lane& l, const Weights& w, int c) {
-#pragma unroll
-        for (int j = 0; j < kSteps; ++j)
-            if ((c * kSteps + j) * 8 + (int)l.vec >= w.KV) r.a[j] = u32x4{0, 0, 0, 0};
-    }
-    template <int NT, int NB>
-    static __device__ __forceinline__ void mma(const Reg (&r)[NT], const u32x4 (&x)[NB][kSteps],
+    // acc += r x over the SN steps from S0 on.
+    template <int S0, int SN, int NT, int NB>
+    static __device__ __forceinline__ void mma(const Reg (&r)[NT], const u32x4 (&x)[NB][SN],
                                                f32x4 (&acc)[NT][NB]) {
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j)
+        for (int j = 0; j < SN; ++j)
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int i = 0; i < NT; ++i) acc[i][b] = mfma(r[i].a[j], x[b][j], acc[i][b]);
+                for (int i = 0; i < NT; ++i) acc[i][b] = mfma(r[i].a[S0 + j], x[b][j], acc[i][b]);
     }
 };
 
@@ -178,6 +175,8 @@ template <bool FP4, int G, bool ZP, bool F16>
 struct PackedWeights {
     static constexpr int kSteps = 4;
     static constexpr int kMaxHeld = 2;
+    static constexpr int kReadWaves = 2;
+    static constexpr bool kWide = G == 128;
     static constexpr int SM = G == 128 ? 2 : 1;  // steps per scale
     static constexpr int GL = kSteps / SM;       // scales per lane, row and chunk
     static constexpr int GP = kPackK / G;        // groups per block
@@ -220,8 +219,6 @@ struct PackedWeights {
             }
         }
     }
-    // Codes and scales past K are zero in the layout.
-    static __device__ __forceinline__ void cut(Reg&, const Lane&, const Weights&, int) {}
     static __device__ __forceinline__ float scale(uint32_t w, int hi) {
         if constexpr (F16) {
             const uint16_t b = (uint16_t)(hi ? w >> 16 : w);
@@ -250,21 +247,22 @@ struct PackedWeights {
         }
         return o;
     }
-    template <int NT, int NB>
-    static __device__ __forceinline__ void mma(const Reg (&r)[NT], const u32x4 (&x)[NB][kSteps],
+    template <int S0, int SN, int NT, int NB>
+    static __device__ __forceinline__ void mma(const Reg (&r)[NT], const u32x4 (&x)[NB][SN],
                                                f32x4 (&acc)[NT][NB]) {
+        static_assert(S0 % SM == 0 && SN % SM == 0, "whole groups");
         constexpr uint32_t kOff = ZP ? 0xc300c300u : 0xc308c308u;  // -128, -136
         const u32x4 off = {kOff, kOff, kOff, kOff};
         const uint32_t k128 = offset_bits();
 #pragma unroll
-        for (int g = 0; g < GL; ++g) {
+        for (int g = S0 / SM; g < (S0 + SN) / SM; ++g) {
             f32x4 x0[NB];
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 x0[b] = f32x4{0, 0, 0, 0};
                 if constexpr (!FP4) {
 #pragma unroll
-                    for (int j = 0; j < SM; ++j) x0[b] = mfma(off, x[b][g * SM + j], x0[b]);
+                    for (int j = 0; j < SM; ++j) x0[b] = mfma(off, x[b][g * SM + j - S0], x0[b]);
                 }
             }
 #pragma unroll
@@ -276,7 +274,7 @@ struct PackedWeights {
                 for (int j = 0; j < SM; ++j) {
                     const u32x4 a = decode(r[i].a[g * SM + j], k128);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) c[b] = mfma(a, x[b][g * SM + j], c[b]);
+                    for (int b = 0; b < NB; ++b) c[b] = mfma(a, x[b][g * SM + j - S0], c[b]);
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -313,22 +311,21 @@ struct PackedWeights {
 template <int TERMS>
 struct Input {
     static constexpr int kRoutes = TERMS == 1 ? 8 : TERMS == 2 ? 4 : 2;
-    uint32_t bytes;  // where the lane's vector of the route's row starts
+    int left;        // vectors of the row from the lane's first on
+    uint32_t bytes;  // where the lane's first vector of the route's row lies
     __device__ __forceinline__ void row(int r, int KV, int lane) {
         const uint32_t term = min((lane & 7) / kRoutes, TERMS - 1);
+        left = KV - lane_vec(lane);
         bytes = (((uint32_t)r * KV + lane_vec(lane)) * TERMS + term) * 16u;
     }
-    template <int STEPS>
+    // Chunk c in chunks of STEPS steps; WHOLE: rows are whole chunks.
+    template <bool WHOLE, int STEPS>
     __device__ __forceinline__ void load(u32x4 (&x)[STEPS], Buffer b, int c) const {
 #pragma unroll
         for (int j = 0; j < STEPS; ++j)
-            x[j] = buffer_load<u32x4, 0>(b, bytes + j * (128 * TERMS), c * (STEPS * 128 * TERMS));
-    }
-    template <int STEPS>
-    static __device__ __forceinline__ void cut(u32x4 (&x)[STEPS], int c, int KV, int lane) {
-#pragma unroll
-        for (int j = 0; j < STEPS; ++j)
-            if ((c * STEPS + j) * 8 + lane_vec(lane) >= KV) x[j] = u32x4{0, 0, 0, 0};
+            x[j] = buffer_load<u32x4, 0>(
+                b, WHOLE || (c * STEPS + j) * 8 < left ? bytes + j * (128 * TERMS) : kPast,
+                c * (STEPS * 128 * TERMS));
     }
     // The wanted sum of a lane i < kRoutes, q < 2: both halves of the inputs
     // and all terms.
@@ -340,6 +337,9 @@ struct Input {
         return o;
     }
 };
+
+// Inputs of a row of h, padded with zeros.
+__host__ __device__ __forceinline__ int padded(int I) { return (I + kPackK - 1) / kPackK * kPackK; }
 
 template <class W>
 __host__ __device__ __forceinline__ int chunks(int K) {
@@ -364,22 +364,15 @@ __device__ __forceinline__ void stream(const Weights& w, const typename W::Ptr (
 #pragma unroll
         for (int i = 0; i < NT; ++i) W::load(r[d][i], wp[i], l, c);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) xp[b].load(x[d][b], xb, c);
+        for (int b = 0; b < NB; ++b) xp[b].template load<false>(x[d][b], xb, c);
     };
-    const int full = w.KV / (W::kSteps * 8);  // the chunk that K cuts, if any
 #pragma unroll
     for (int d = 0; d < D - 1; ++d) load(d, lo + d);
     for (int c = lo;;) {
 #pragma unroll
         for (int d = 0; d < D; ++d) {
             load((d + D - 1) % D, c + D - 1);
-            if (c == full) {
-#pragma unroll
-                for (int i = 0; i < NT; ++i) W::cut(r[d][i], l, w, c);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) Input<TERMS>::cut(x[d][b], c, w.KV, lane);
-            }
-            W::template mma<NT, NB>(r[d], x[d], acc);
+            W::template mma<0, W::kSteps, NT, NB>(r[d], x[d], acc);
             if (++c >= hi) return;
         }
     }
@@ -398,7 +391,7 @@ struct RowsArgs {
     void* out;           // [n, N] bf16 or fp32
     int out_f32;
     // first half of the layer
-    u32x4* h;            // [n][I / 8][terms]
+    u32x4* h;            // [n][padded(I) / 8][terms]
     int I, terms;
     Table* table;
 };
@@ -518,8 +511,12 @@ struct Finder {
             t->offset[s0] = off;
         }
     }
-    __device__ __forceinline__ void write_routes(Table* t, int off, int cnt) const {
-        for (int i = threadIdx.x; i < cnt; i += blockDim.x) t->route[off + i] = list[i];
+    // (and the zeros that pad its routes' rows of h)
+    __device__ __forceinline__ void write_routes(const RowsArgs& a, int off, int cnt) const {
+        for (int i = threadIdx.x; i < cnt; i += blockDim.x) a.table->route[off + i] = list[i];
+        const int row = padded(a.I) / 8 * a.terms, from = a.I / 8 * a.terms, pad = row - from;
+        for (int i = threadIdx.x; i < cnt * pad; i += blockDim.x)
+            a.h[(size_t)list[i / pad] * row + from + i % pad] = u32x4{0, 0, 0, 0};
     }
 };
 
@@ -533,7 +530,7 @@ __device__ __forceinline__ void store_rows(const RowsArgs& a, int r, int row, f3
         float h[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[k] = silu(v[k]) * up[k];
-        u32x2* dst = (u32x2*)(a.h + ((size_t)r * (a.I / 8) + row / 8) * a.terms) + (row % 8) / 4;
+        u32x2* dst = (u32x2*)(a.h + ((size_t)r * (padded(a.I) / 8) + row / 8) * a.terms) + (row % 8) / 4;
         for (int n = 0; n < a.terms; ++n) {
             const u32x2 o = {bf16x2_bits(h[0], h[1]), bf16x2_bits(h[2], h[3])};
             dst[2 * n] = o;
@@ -581,7 +578,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void expert_rows_held(const RowsA
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x) / kWave;
     const int nw = blockDim.x / kWave;
-    const int KC = chunks<W>(a.w.K), full = a.w.KV / (W::kSteps * 8);
+    const int KC = chunks<W>(a.w.K);
     const int ck0 = wave * XC;
     const Buffer xb = buffer_of(a.x, (uint32_t)(a.n / a.div) * a.w.KV * 16u);
     const typename W::Lane l = W::lane_of(a.w, lane);
@@ -607,7 +604,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void expert_rows_held(const RowsA
                 cnt = s_find.find(a, e, &off);
                 found = e;
                 if constexpr (LAYER) {
-                    if (g0 == 0 && c0 == 0) s_find.write_routes(a.table, off, cnt);
+                    if (g0 == 0 && c0 == 0) s_find.write_routes(a, off, cnt);
                 }
             }
         }
@@ -619,7 +616,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void expert_rows_held(const RowsA
         xp.row((a.ids ? s_find.list[jx] : jx) / a.div, a.w.KV, lane);
         any_of<XC>([&](auto j) MEP_INLINE {
             const int c = min(ck0 + j, KC - 1);
-            xp.load(x[j][0], xb, c);
+            xp.template load<false>(x[j][0], xb, c);
             return false;
         });
         auto load = [&](int g, auto i) MEP_INLINE {
@@ -633,8 +630,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void expert_rows_held(const RowsA
             acc[i][0][0] = f32x4{0, 0, 0, 0};
             any_of<XC>([&](auto j) MEP_INLINE {
                 if (ck0 + j < KC) {
-                    if (ck0 + j == full) W::cut(r[i][j][0], l, a.w, full);
-                    W::template mma<1, 1>(r[i][j], x[j], acc[i]);
+                    W::template mma<0, W::kSteps, 1, 1>(r[i][j], x[j], acc[i]);
                 }
                 return false;
             });
@@ -675,10 +671,6 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void expert_rows_held(const RowsA
         };
         any_of<NT - 1>([&](auto i) MEP_INLINE {
             load(g0, i);
-            return false;
-        });
-        any_of<XC>([&](auto j) MEP_INLINE {
-            if (ck0 + j >= full) Input<1>::cut(x[j][0], ck0 + j, a.w.KV, lane);
             return false;
         });
         for (int g = g0; g + 1 < g1; ++g) {
@@ -758,7 +750,7 @@ __device__ __forceinline__ void rows_pass(const RowsArgs& a, const Finder& find,
 }
 
 template <class W, bool LAYER, int RT, int NW>
-__global__ __launch_bounds__(NW* kWave, RD_WPE) void expert_rows_read(const RowsArgs a) {
+__global__ __launch_bounds__(NW* kWave, W::kReadWaves) void expert_rows_read(const RowsArgs a) {
     __shared__ Finder s_find;
     __shared__ f32x4 s_part[NW * (LAYER ? 2 : 1) * RT * 2 * 32];
     const int row0 = blockIdx.x * (RT * kTile);
@@ -782,7 +774,7 @@ __global__ __launch_bounds__(NW* kWave, RD_WPE) void expert_rows_read(const Rows
         int off;
         cnt = s_find.find(a, e, &off);
         if constexpr (LAYER) {
-            if (blockIdx.x == 0) s_find.write_routes(a.table, off, cnt);
+            if (blockIdx.x == 0) s_find.write_routes(a, off, cnt);
         }
     }
     const Buffer xb = buffer_of(a.x, (uint32_t)(a.n / a.div) * a.w.KV * 16u);
@@ -822,7 +814,7 @@ struct Job {
 // visits; the waves' sums are joined in wave order at the end. Every sum has
 // a fixed order, so equal inputs give equal bits.
 template <class W, int TERMS, int RT, int NW>
-__global__ __launch_bounds__(NW* kWave, DN_WPE) void expert_down(const DownArgs a) {
+__global__ __launch_bounds__(NW* kWave, 2) void expert_down(const DownArgs a) {
     extern __shared__ f32x4 s_dyn[];
     __shared__ int s_jobs;
     constexpr int R4 = RT * 2;  // row quads
@@ -865,21 +857,26 @@ __global__ __launch_bounds__(NW* kWave, DN_WPE) void expert_down(const DownArgs 
     }
     lds_barrier();
 
-    const int KC = chunks<W>(a.w.K), full = a.w.KV / (W::kSteps * 8);
-    const long long steps = (long long)s_jobs * KC;
+    const int KC = chunks<W>(a.w.K);
+    const long long steps = (long long)__builtin_amdgcn_readfirstlane(s_jobs) * KC;
     const int lo = (int)(steps * wave / NW), hi = (int)(steps * (wave + 1) / NW);
     f32x4* sum = s_sum + (size_t)wave * a.T * R4;
-    const Buffer hb = buffer_of(a.h, (uint32_t)a.n * a.w.KV * (TERMS * 16u));
+    const int hv = padded(a.w.K) / 8;  // vectors of a row of h
+    const Buffer hb = buffer_of(a.h, (uint32_t)a.n * hv * (TERMS * 16u));
     const typename W::Lane l = W::lane_of(a.w, lane);
 
     if (lo < hi) {
+        // Weights are loaded a chunk ahead, inputs half a chunk (they come
+        // from the caches, and a whole chunk of two blocks twice would take
+        // half the registers).
+        constexpr int HS = W::kSteps / 2;
         typename W::Reg r[2][RT];
-        u32x4 x[2][2][W::kSteps];
+        u32x4 x[2][2][HS];  // [half][block]
         f32x4 acc[RT][2];
 #pragma unroll
         for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
         struct At {
-            int job, chunk, blocks;
+            int job, chunk, two;
         };
         typename W::Ptr wp[RT];
         Input<TERMS> xp[2];
@@ -892,27 +889,21 @@ __global__ __launch_bounds__(NW* kWave, DN_WPE) void expert_down(const DownArgs 
 #pragma unroll
             for (int b = 0; b < 2; ++b)
                 xp[b].row(s_route[j.off + min(b * kRoutes + (lane & (kRoutes - 1)), cnt - 1)],
-                          a.w.KV, lane);
-            p.blocks = cnt > kRoutes ? 2 : 1;
+                          hv, lane);
+            p.two = cnt > kRoutes;
         };
-        auto load = [&](int d, const At& p) MEP_INLINE {
-            xp[0].load(x[d][0], hb, p.chunk);
+        auto load_w = [&](auto d, const At& p) MEP_INLINE {
 #pragma unroll
             for (int i = 0; i < RT; ++i) W::load(r[d][i], wp[i], l, p.chunk);
-            if (p.blocks == 2) xp[1].load(x[d][1], hb, p.chunk);
         };
-        auto next = [&](At& p) MEP_INLINE {
-            if (++p.chunk == KC) {
-                p.chunk = 0;
-                ++p.job;
-                open(p);
-            }
+        auto load_x = [&](auto h, const At& p) MEP_INLINE {
+            xp[0].template load<true>(x[h][0], hb, p.chunk * 2 + h);
+            if (p.two) xp[1].template load<true>(x[h][1], hb, p.chunk * 2 + h);
         };
-        auto fold = [&](int job) MEP_INLINE {  // adds the sums of a job's routes to their tokens'
+        auto fold = [&](int job) MEP_INLINE {  // adds a job's sums to its tokens'
             const Job j = s_job[job];
             const int cnt = __builtin_amdgcn_readfirstlane(j.cnt);
-            const int blocks = cnt > kRoutes ? 2 : 1;
-            for (int b = 0; b < blocks; ++b) {
+            any_of<2>([&](auto b) MEP_INLINE {
                 const int c = b * kRoutes + (lane & (kRoutes - 1));
                 bool todo = lane < 32 && (lane & 15) < kRoutes && c < cnt;
                 const int tok = s_token[j.off + min(c, cnt - 1)];
@@ -921,8 +912,7 @@ __global__ __launch_bounds__(NW* kWave, DN_WPE) void expert_down(const DownArgs 
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[i][k] = Input<TERMS>::total(b ? acc[i][1][k] : acc[i][0][k], lane);
+                    for (int k = 0; k < 4; ++k) v[i][k] = Input<TERMS>::total(acc[i][b][k], lane);
                 // a token that names an expert twice has adjacent columns:
                 // they are added one after the other
                 while (__ballot(todo)) {
@@ -939,51 +929,46 @@ __global__ __launch_bounds__(NW* kWave, DN_WPE) void expert_down(const DownArgs 
                         todo = false;
                     }
                 }
-            }
+                return cnt <= kRoutes;
+            });
 #pragma unroll
             for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
         };
-        auto use = [&](int d, const At& p, bool last) MEP_INLINE {
-            if (p.chunk == full) {
-#pragma unroll
-                for (int i = 0; i < RT; ++i) W::cut(r[d][i], l, a.w, full);
-                Input<TERMS>::cut(x[d][0], full, a.w.KV, lane);
-                Input<TERMS>::cut(x[d][1], full, a.w.KV, lane);
-            }
-            if (p.blocks == 2) {
-                W::template mma<RT, 2>(r[d], x[d], acc);
-            } else {
-                u32x4(&x1)[1][W::kSteps] = reinterpret_cast<u32x4(&)[1][W::kSteps]>(x[d][0]);
-                f32x4 one[RT][1];
-#pragma unroll
-                for (int i = 0; i < RT; ++i) one[i][0] = acc[i][0];
-                W::template mma<RT, 1>(r[d], x1, one);
-#pragma unroll
-                for (int i = 0; i < RT; ++i) acc[i][0] = one[i][0];
-            }
-            if (last || p.chunk == KC - 1) fold(p.job);
+        // Both blocks are always multiplied (the second's inputs are stale
+        // where a job has one, and its sums not used): a branch here costs
+        // more than the matrix cores' time.
+        auto use = [&](auto d, auto h) MEP_INLINE {
+            W::template mma<h * HS, HS, RT, 2>(r[d], x[h], acc);
         };
-        At p[2];
-        p[0] = {lo / KC, lo % KC, 1};
-        open(p[0]);
-        load(0, p[0]);
-        for (int s = lo;; ++s) {
+        constexpr std::integral_constant<int, 0> k0{};
+        constexpr std::integral_constant<int, 1> k1{};
+        At cur = {lo / KC, lo % KC, 0};
+        open(cur);
+        load_w(k0, cur);
+        load_x(k0, cur);
+        int s = lo;
+        while (!any_of<2>([&](auto d) MEP_INLINE {
+            load_x(k1, cur);
             if (s + 1 >= hi) {
-                use(0, p[0], true);
-                break;
+                use(d, k0);
+                use(d, k1);
+                fold(cur.job);
+                return true;
             }
-            p[1] = p[0];
-            next(p[1]);
-            load(1, p[1]);
-            use(0, p[0], false);
-            if (++s + 1 >= hi) {
-                use(1, p[1], true);
-                break;
+            At nxt = {cur.job, cur.chunk + 1, cur.two};
+            if (nxt.chunk == KC) {
+                nxt = {cur.job + 1, 0, 0};
+                open(nxt);
             }
-            p[0] = p[1];
-            next(p[0]);
-            load(0, p[0]);
-            use(1, p[1], false);
+            load_w(std::integral_constant<int, 1 - d>{}, nxt);
+            use(d, k0);
+            load_x(k0, nxt);
+            use(d, k1);
+            if (nxt.chunk == 0) fold(cur.job);
+            cur = nxt;
+            ++s;
+            return false;
+        })) {
         }
     }
     lds_barrier();
@@ -1021,10 +1006,6 @@ inline int tiles_of(int rows, int rt) { return (rows + rt * kTile - 1) / (rt * k
 #define READ_RT 2
 #define READ_NW 4
 #endif
-#ifndef DN_RT
-#define DN_RT 2
-#define DN_NW 4
-#endif
 
 template <class W, bool LAYER, int NT, int XC>
 void launch_held(hipStream_t s, const RowsArgs& a, int kc) {
@@ -1060,10 +1041,23 @@ inline size_t down_lds(int nw, int rt, int T, int n) {
     return (size_t)nw * T * rt * 2 * 16 + (size_t)n * (8 + 4 + 2 + 1) + 16;
 }
 
+#ifndef DN_SRT
+#define DN_SRT 2
+#define DN_SNW 8
+#endif
+template <class W, int TERMS, int RT, int NW>
+void launch_down(hipStream_t s, const DownArgs& d) {
+    hipLaunchKernelGGL((expert_down<W, TERMS, RT, NW>), dim3(tiles_of(d.w.N, RT)),
+                       dim3(NW * kWave), down_lds(NW, RT, d.T, d.n), s, d);
+}
+
 template <class W, int TERMS>
 void launch_down(hipStream_t s, const DownArgs& d) {
-    hipLaunchKernelGGL((expert_down<W, TERMS, DN_RT, DN_NW>), dim3(tiles_of(d.w.N, DN_RT)),
-                       dim3(DN_NW * kWave), down_lds(DN_NW, DN_RT, d.T, d.n), s, d);
+    if constexpr (W::kWide) {
+        if (d.T <= 32 && tiles_of(d.w.N, 4) >= kCus * 3 / 4) return launch_down<W, TERMS, 4, 8>(s, d);
+    }
+    if (d.T <= 64) return launch_down<W, TERMS, DN_SRT, DN_SNW>(s, d);
+    launch_down<W, TERMS, 2, 4>(s, d);
 }
 
 template <class W>

@@ -88,7 +88,7 @@ extern "C" size_t mep_moe_layer_workspace_size(int T, int K, int I) {
     if (T < 0 || T > kMaxLayerTokens || K < 1 || (long long)T * K > kMaxRoutes || I < 8 ||
         I > kMaxDim || I % 8 != 0)
         return 0;
-    return table_bytes() + (size_t)T * K * I * 2 * 3;  // up to 3 bf16 terms
+    return table_bytes() + (size_t)T * K * padded(I) * 2 * 3;  // up to 3 bf16 terms
 }
 
 extern "C" int mep_moe_layer(int T, int K, int H, int I, int first, const uint16_t* x,

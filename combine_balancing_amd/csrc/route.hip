@@ -12,7 +12,8 @@
 //   ids = the K largest c, descending; ties go to the lower id
 //   w = s[ids], renormalised to sum 1 if asked, times `scale`
 // A choice next to a border must not hang on how s was rounded, so c is
-// formed and compared in fp64.
+// formed in fp64, and groups are compared in it; experts are compared on the
+// upper 42 bits of c's mantissa, whose lower bits carry the expert's id.
 #include <algorithm>
 
 #include "rows.h"
@@ -25,6 +26,7 @@ constexpr int kRouteWaves = kRouteThreads / kWave;
 constexpr int kRouteMaxE = 1024;
 constexpr int kRouteMaxK = 64;  // one lane per chosen expert
 constexpr int kRouteMaxGroups = 64;
+constexpr int kRouteManyTokens = 4096;
 constexpr double kRenormEps = 1e-20;  // sigmoid scores may all round to zero
 
 template <typename T>
@@ -66,7 +68,219 @@ __device__ __forceinline__ double wave_sum_d(double v) {
     return v;
 }
 
-// One wave per token; lane i holds experts i, i + 64, ... (V of them).
+// exp(x) for x <= 0 within about 2^-50 (0 below -800): 2^n times the Taylor
+// series of the remainder r = x - n ln 2, |r| <= ln(2) / 2, to the 13th power
+// (the next term is under 5e-18). ln 2 is taken in two parts, the first with
+// 40 fraction bits, so that n times it is exact.
+__device__ __forceinline__ double exp_neg(double x) {
+    x = fmax(x, -800.0);
+    const double n = rint(x * 1.4426950408889634);
+    double r = __builtin_fma(n, -0.6931471805601177, x);
+    r = __builtin_fma(n, 1.7239444525614835e-13, r);
+    double p = 1.0 / 6227020800.0;
+    p = __builtin_fma(p, r, 1.0 / 479001600.0);
+    p = __builtin_fma(p, r, 1.0 / 39916800.0);
+    p = __builtin_fma(p, r, 1.0 / 3628800.0);
+    p = __builtin_fma(p, r, 1.0 / 362880.0);
+    p = __builtin_fma(p, r, 1.0 / 40320.0);
+    p = __builtin_fma(p, r, 1.0 / 5040.0);
+    p = __builtin_fma(p, r, 1.0 / 720.0);
+    p = __builtin_fma(p, r, 1.0 / 120.0);
+    p = __builtin_fma(p, r, 1.0 / 24.0);
+    p = __builtin_fma(p, r, 1.0 / 6.0);
+    p = __builtin_fma(p, r, 0.5);
+    p = __builtin_fma(p, r, 1.0);
+    p = __builtin_fma(p, r, 1.0);
+    return __builtin_ldexp(p, (int)n);
+}
+
+// 1 / d for 1 <= d <= 2: the hardware's estimate and two Newton steps.
+__device__ __forceinline__ double reciprocal(double d) {
+    double y = __builtin_amdgcn_rcp(d);
+    y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+    return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+}
+
+__device__ __forceinline__ double sigmoid(float l) {
+    const double x = exp_neg(-fabs((double)l));
+    const double y = reciprocal(1.0 + x);
+    return l >= 0.0f ? y : x * y;
+}
+
+// Exchange of a double over the L lanes (16, 32 or 64) of a token: within 16
+// by row rotations (no LDS), further by shuffles.
+template <int CTRL>
+__device__ __forceinline__ double row_move(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)u, CTRL, 0xf, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, 0xf, 0xf, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+template <int L, class F>
+__device__ __forceinline__ double lanes_reduce(double v, F f) {
+    v = f(v, row_move<0x128>(v));  // row_ror 8, 4, 2, 1
+    v = f(v, row_move<0x124>(v));
+    v = f(v, row_move<0x122>(v));
+    v = f(v, row_move<0x121>(v));
+    if (L >= 32) v = f(v, __shfl_xor(v, 16, kWave));
+    if (L >= 64) v = f(v, __shfl_xor(v, 32, kWave));
+    return v;
+}
+template <int L>
+__device__ __forceinline__ double lanes_max(double v) {
+    return lanes_reduce<L>(v, [](double a, double b) { return fmax(a, b); });
+}
+template <int L>
+__device__ __forceinline__ double lanes_sum(double v) {
+    return lanes_reduce<L>(v, [](double a, double b) { return a + b; });
+}
+
+constexpr double kNone = -1e300;  // an expert that cannot be taken (c is above -1e39)
+
+// L lanes per token; lane i of them holds experts i * V .. i * V + V - 1.
+// Needs E <= L * V, K <= L, and whole lanes per group.
+//
+// The chosen are taken one by one: the largest of a lane's V values, the
+// largest over the lanes, and the value is struck from the lane that has it.
+// The id in a value's lowest 10 bits (complemented where the value is
+// positive) makes all values different and equal c go to the lower id, so a
+// maximum is all it takes. 64 / L tokens share a wave: the exchange over the
+// lanes then serves several tokens, and V = 16 leaves most of a step to the
+// plain maxima of a lane. 32768 tokens over 256 experts, bias and groups:
+// see the launch.
+template <typename LT, int L, int V>
+__global__ __launch_bounds__(kRouteThreads) void route_lanes(
+    const LT* __restrict__ logits, const float* __restrict__ bias, int sig, int wide, int n_group,
+    int topk_group, int renorm, float scale, int* __restrict__ ids, float* __restrict__ scores,
+    int T, int E, int K) {
+    constexpr int kTokens = kRouteThreads / L;
+    const int lane = lane_id(), i = lane & (L - 1), base = lane & ~(L - 1);
+    const int t_raw = blockIdx.x * kTokens + threadIdx.x / L;
+    const int t = min(t_raw, T - 1);  // lanes past T work on a real row, store nothing
+    const LT* row = logits + (size_t)t * E;
+
+    float l[V];
+    if (wide) {  // rows and lanes start on 16 bytes, E is a multiple of V
+        constexpr int N = 16 / sizeof(LT), M = V < N ? V : N;
+        typedef LT vec __attribute__((ext_vector_type(M)));
+#pragma unroll
+        for (int v = 0; v < V; v += M) {
+            const vec w = *(const vec*)(row + min(i * V, E - V) + v);
+#pragma unroll
+            for (int k = 0; k < M; ++k) l[v + k] = widen<LT>(w[k]);
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = widen<LT>(row[min(i * V + v, E - 1)]);
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        l[v] = i * V + v < E ? clean(l[v]) : -INFINITY;
+        top = fmaxf(top, l[v]);
+    }
+    double z = 1.0;  // 1 / sum of the softmax
+    if (!sig) {
+        top = (float)lanes_max<L>(top);
+        if (bias || !renorm) {
+            double part = 0.0;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                part += l[v] > -INFINITY ? exp_neg((double)l[v] - (double)top) : 0.0;
+            part = lanes_sum<L>(part);
+            z = part > 0.0 ? 1.0 / part : 0.0;
+        }
+    }
+
+    double c[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        c[v] = (double)l[v] + 0.0;  // -0 counts as 0
+        if (bias) {
+            const double s = sig ? sigmoid(l[v]) : exp_neg((double)l[v] - (double)top) * z;
+            c[v] = s + (double)bias[min(i * V + v, E - 1)];
+        }
+        if (!(l[v] > -INFINITY && c[v] > kNone)) c[v] = kNone;  // absent, or a bias of -inf or NaN
+        c[v] = fmin(c[v], 1e300);
+    }
+
+    if (n_group > 1) {
+        double a = kNone, b = kNone;  // the two largest of the lane, then of the group
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            b = fmax(b, fmin(a, c[v]));
+            a = fmax(a, c[v]);
+        }
+        const int per = E / n_group / V;  // lanes of a group
+        const int mine = i / per, first = base + min(mine, n_group - 1) * per;
+        double ga = kNone, gb = kNone;
+        for (int j = 0; j < per; ++j) {
+            const double oa = __shfl(a, first + j, kWave), ob = __shfl(b, first + j, kWave);
+            gb = fmax(fmax(gb, ob), fmin(ga, oa));
+            ga = fmax(ga, oa);
+        }
+        const double gv = bias && gb > kNone ? ga + gb : ga;
+        int rank = 0;
+        for (int j = 0; j < n_group; ++j) {
+            const double o = __shfl(gv, base + j * per, kWave);
+            rank += o > gv || (o == gv && j < mine);
+        }
+        if (rank >= topk_group) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) c[v] = kNone;
+        }
+    }
+
+    // the id in the lowest bits
+    uint32_t hi[V], lo[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const uint64_t u = __builtin_bit_cast(uint64_t, c[v]);
+        hi[v] = (uint32_t)(u >> 32);
+        const uint32_t flip = ~(uint32_t)((int)hi[v] >> 31) & (kRouteMaxE - 1);
+        lo[v] = ((uint32_t)u & ~(uint32_t)(kRouteMaxE - 1)) | ((uint32_t)(i * V + v) ^ flip);
+    }
+    auto value = [&](int v) {
+        return __builtin_bit_cast(double, ((uint64_t)hi[v] << 32) | lo[v]);
+    };
+    constexpr uint32_t kNoneHi = (uint32_t)(__builtin_bit_cast(uint64_t, kNone) >> 32);
+    int my_id = -1;
+    for (int k = 0; k < K; ++k) {
+        double best = value(0);
+#pragma unroll
+        for (int v = 1; v < V; ++v) best = fmax(best, value(v));
+        best = lanes_max<L>(best);
+        const uint64_t u = __builtin_bit_cast(uint64_t, best);
+        const uint32_t low = (uint32_t)u & (kRouteMaxE - 1);
+        const int id = (int)(best < 0.0 ? low : low ^ (kRouteMaxE - 1));
+        if (i == k && best > 0.5 * kNone) my_id = id;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (i * V + v == id) hi[v] = kNoneHi;
+    }
+
+    const float my_l = my_id >= 0 ? clean(widen<LT>(row[my_id])) : -INFINITY;
+    double s = 0.0;
+    if (sig) {
+        s = my_id >= 0 ? sigmoid(my_l) : 0.0;
+        if (renorm) s = s / (lanes_sum<L>(s) + kRenormEps);
+    } else if (renorm) {  // the softmax of the chosen
+        const double m = lanes_max<L>(my_id >= 0 ? (double)my_l : kNone);
+        s = my_id >= 0 ? exp_neg((double)my_l - m) : 0.0;
+        const double d = lanes_sum<L>(s);
+        s = d > 0.0 ? s / d : 0.0;
+    } else {
+        s = my_id >= 0 ? exp_neg((double)my_l - (double)top) * z : 0.0;
+    }
+    if (t_raw < T && i < K) {
+        ids[(size_t)t * K + i] = my_id;
+        scores[(size_t)t * K + i] = (float)(s * (double)scale);
+    }
+}
+
+// Any shape: one wave per token; lane i holds experts i, i + 64, ... (V of
+// them). For groups that do not consist of whole lanes of route_lanes.
 template <typename LT, int V, bool SIGMOID>
 __global__ __launch_bounds__(kRouteThreads) void route_rows(
     const LT* __restrict__ logits, const float* __restrict__ bias, int n_group, int topk_group,
@@ -268,9 +482,37 @@ void launch_route(hipStream_t s, bool sig, const void* logits, const float* bias
                            renorm, scale, ids, scores, T, E, K);
 }
 
+template <typename LT, int L, int V>
+bool try_lanes(hipStream_t s, bool sig, const void* logits, const float* bias, int ng, int tg,
+               int renorm, float scale, int* ids, float* scores, int T, int E, int K) {
+    if (E > L * V || K > L || (ng > 1 && (E / ng) % V != 0)) return false;
+    constexpr size_t kVec = V * sizeof(LT) < 16 ? V * sizeof(LT) : 16;
+    const int wide = E % V == 0 && (E * sizeof(LT)) % kVec == 0 && (uintptr_t)logits % kVec == 0;
+    constexpr int kTokens = kRouteThreads / L;
+    hipLaunchKernelGGL((route_lanes<LT, L, V>), dim3((T + kTokens - 1) / kTokens),
+                       dim3(kRouteThreads), 0, s, (const LT*)logits, bias, sig ? 1 : 0, wide, ng,
+                       tg, renorm, scale, ids, scores, T, E, K);
+    return true;
+}
+
 template <typename LT>
 void dispatch_route(hipStream_t s, bool sig, const void* logits, const float* bias, int ng, int tg,
                     int renorm, float scale, int* ids, float* scores, int T, int E, int K) {
+#define MEP_TRY(L, V)                                                                          \
+    if (try_lanes<LT, L, V>(s, sig, logits, bias, ng, tg, renorm, scale, ids, scores, T, E, K)) \
+        return;
+    if (T >= kRouteManyTokens) {
+        MEP_TRY(16, 4)
+        MEP_TRY(16, 8)
+        MEP_TRY(16, 16)
+        MEP_TRY(32, 12)
+        MEP_TRY(32, 16)
+    }
+    MEP_TRY(64, 4)
+    MEP_TRY(64, 8)
+    MEP_TRY(64, 12)
+    MEP_TRY(64, 16)
+#undef MEP_TRY
     if (E <= 256)
         launch_route<LT, 4>(s, sig, logits, bias, ng, tg, renorm, scale, ids, scores, T, E, K);
     else if (E <= 512)
