@@ -110,10 +110,14 @@ __device__ __forceinline__ int lane_vec(int lane) { return (lane >> 4) + ((lane 
 // part of one 8-row tile starts), Reg (one chunk of it in registers), load,
 // and mma (chunk times NB column blocks).
 
+// WHOLE: K is a multiple of a chunk. Otherwise, in the chunk that K cuts, a
+// lane's vectors past K lie in the next row and are loaded from past the
+// buffer, as zeros; the selects this takes cost 4 us of 80 on 7168 inputs.
+template <bool WHOLE>
 struct Bf16Weights {
     static constexpr int kSteps = 2;
     static constexpr int kMaxHeld = 4;    // chunks of inputs that a wave can hold
-    static constexpr int kReadWaves = 4;  // waves per SIMD that expert_rows_read is built for
+    static constexpr int kReadWaves = 2;  // waves per SIMD that expert_rows_read is built for
     static constexpr bool kWide = true;   // whether expert_down takes four tiles at a time
     struct Reg {
         u32x4 a[kSteps];
@@ -133,13 +137,12 @@ struct Bf16Weights {
         const u32x4* p = w.codes + ((size_t)e * w.N + min(row0, w.N - kTile)) * w.KV;
         return {buffer_of(p, (uint32_t)(kTile * w.KV) * 16u)};
     }
-    // In the chunk that K cuts, a lane's vectors past K lie in the next row:
-    // they are loaded from past the buffer, as zeros.
     static __device__ __forceinline__ void load(Reg& r, const Ptr& p, const Lane& l, int c) {
 #pragma unroll
         for (int j = 0; j < kSteps; ++j)
             r.a[j] = buffer_load<u32x4, kNt>(
-                p.rows, (c * kSteps + j) * 8 < l.left ? l.bytes + j * 128 : kPast,
+                p.rows,
+                WHOLE || (c * kSteps + j) * 8 < l.left ? l.bytes + j * 128 : kPast,
                 c * (kSteps * 128));
     }
     // acc += r x over the SN steps from S0 on.
@@ -396,9 +399,43 @@ struct RowsArgs {
     Table* table;
 };
 
-// The experts that any route reaches ("slots", ascending), jobs of up to 8
-// of an expert's routes, and an expert's routes in route order. All threads
-// of the work-group take part in each call.
+// Up to 64 routes, one per lane: every wave finds experts and routes by
+// itself in registers, with no barrier (the decode of a few tokens is mostly
+// waiting). Experts are ordered by their first route.
+struct FewRoutes {
+    int id;          // this lane's expert, or -1
+    uint64_t peers;  // the lanes of that expert
+    int first;       // the lowest of them (64 where id is -1)
+
+    static __device__ __forceinline__ FewRoutes read(const int* ids, const uint8_t* mask, int n,
+                                                     int first_id, int E) {
+        FewRoutes f;
+        const int lane = lane_id();
+        f.id = -1;
+        if (lane < n) {
+            // in 64 bits: an id far outside may not wrap into the range
+            const long long v = (long long)ids[lane] - first_id;
+            if (v >= 0 && v < E && !(mask && mask[lane] == 0)) f.id = (int)v;
+        }
+        f.peers = match_peers<kKeyBits>(f.id, f.id >= 0);
+        f.first = f.id >= 0 ? (int)__builtin_ctzll(f.peers) : kWave;
+        return f;
+    }
+    // Jobs of `per` routes: a lane that is its expert's first gets the number
+    // of its expert's jobs, other lanes 0.
+    __device__ __forceinline__ int jobs(int per) const {
+        return first == lane_id() ? (__popcll(peers) + per - 1) / per : 0;
+    }
+    // This route's place in a list ordered by (expert's first route, route).
+    __device__ __forceinline__ int place() const {
+        const int ends = wave_inclusive_sum(first == lane_id() ? __popcll(peers) : 0);
+        return __shfl(ends, first & (kWave - 1), kWave) - __popcll(peers) + count_below(peers);
+    }
+};
+
+// The experts that any route reaches, jobs of up to 8 of an expert's routes,
+// and an expert's routes in route order. All threads of the work-group take
+// part in each call.
 struct Finder {
     int16_t id[kMaxRoutes];
     uint16_t list[kMaxRoutes];
@@ -408,8 +445,12 @@ struct Finder {
     int count[kMaxWaves], less[kMaxWaves], slots, jobs;
 
     // Reads the ids; returns the number of jobs.
-    __device__ __forceinline__ int begin(const RowsArgs& a) {
+    __device__ __forceinline__ int begin(const RowsArgs& a, FewRoutes& few) {
         const int tid = threadIdx.x;
+        if (a.n <= kWave) {
+            few = FewRoutes::read(a.ids, a.mask, a.n, a.first, a.E);
+            return __builtin_amdgcn_readlane(wave_inclusive_sum(few.jobs(kCols)), kWave - 1);
+        }
         // counted in pairs of 16 bits: no more than 2048 routes
         uint32_t* pairs = (uint32_t*)routes;
         for (int i = tid; i < kMaxExperts / 2; i += blockDim.x) pairs[i] = 0u;
@@ -445,15 +486,32 @@ struct Finder {
         return __builtin_amdgcn_readfirstlane(jobs);
     }
 
-    __device__ __forceinline__ int expert_of(int j, int* c0) const {
+    // Expert of a job, and the job's first place among that expert's routes.
+    __device__ __forceinline__ int expert_of(const RowsArgs& a, const FewRoutes& few, int j,
+                                             int* c0) const {
+        if (a.n <= kWave) {
+            const int mine = few.jobs(kCols), to = wave_inclusive_sum(mine);
+            const int at = (int)__builtin_ctzll(__ballot(j < to && j >= to - mine));
+            *c0 = (j - (__builtin_amdgcn_readlane(to, at) - __builtin_amdgcn_readlane(mine, at))) *
+                  kCols;
+            return __builtin_amdgcn_readlane(few.id, at);
+        }
         *c0 = __builtin_amdgcn_readfirstlane(pass[j]) * kCols;
         return __builtin_amdgcn_readfirstlane(job[j]);
     }
 
     // `list` = the routes of expert e; returns their count. *off: routes of
     // lower experts.
-    __device__ __forceinline__ int find(const RowsArgs& a, int e, int* off_out) {
+    __device__ __forceinline__ int find(const RowsArgs& a, const FewRoutes& few, int e,
+                                        int* off_out) {
         const int lane = lane_id();
+        *off_out = 0;
+        if (a.n <= kWave) {  // each wave writes the same list
+            const uint64_t m = __ballot(few.id == e);
+            if (few.id == e) list[count_below(m)] = (uint16_t)lane;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            return __popcll(m);
+        }
         const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x) / kWave;
         const int nw = blockDim.x / kWave;
         // each wave takes a range of whole 64-route rounds
@@ -488,8 +546,9 @@ struct Finder {
         return __builtin_amdgcn_readfirstlane(routes[e]);
     }
 
-    // What the layer's second kernel reads: the slots, from work-group 0, and
-    // an expert's routes, from the one that has its first rows.
+    // What the layer's second kernel reads where there are more than 64
+    // routes: the slots, from work-group 0, and an expert's routes, from the
+    // work-group that has its first rows.
     __device__ __forceinline__ void write_slots(Table* t) const {
         if (blockIdx.x != 0 || blockIdx.y != 0 || threadIdx.x >= kWave) return;
         const int lane = lane_id();
@@ -513,7 +572,8 @@ struct Finder {
     }
     // (and the zeros that pad its routes' rows of h)
     __device__ __forceinline__ void write_routes(const RowsArgs& a, int off, int cnt) const {
-        for (int i = threadIdx.x; i < cnt; i += blockDim.x) a.table->route[off + i] = list[i];
+        if (a.n > kWave)
+            for (int i = threadIdx.x; i < cnt; i += blockDim.x) a.table->route[off + i] = list[i];
         const int row = padded(a.I) / 8 * a.terms, from = a.I / 8 * a.terms, pad = row - from;
         for (int i = threadIdx.x; i < cnt * pad; i += blockDim.x)
             a.h[(size_t)list[i / pad] * row + from + i % pad] = u32x4{0, 0, 0, 0};
@@ -586,8 +646,11 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void expert_rows_held(const RowsA
     const bool wanted = (i16 < 8) == (q < 2);
     const int part = (q >> 1) * 16 + (q & 1) * 8 + (i16 & 7);
 
-    const int total = a.ids ? s_find.begin(a) : (a.n + kCols - 1) / kCols;
-    if constexpr (LAYER) s_find.write_slots(a.table);
+    FewRoutes few = {};
+    const int total = a.ids ? s_find.begin(a, few) : (a.n + kCols - 1) / kCols;
+    if constexpr (LAYER) {
+        if (a.n > kWave) s_find.write_slots(a.table);
+    }
     const long long items = (long long)total * groups;
     const long long end = items * (blockIdx.x + 1) / gridDim.x;
     int turn = 0, found = -1, cnt = a.n;
@@ -597,11 +660,11 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void expert_rows_held(const RowsA
         at += g1 - g0;
         int e = 0, c0 = job * kCols;
         if (a.ids) {
-            e = s_find.expert_of(job, &c0);
+            e = s_find.expert_of(a, few, job, &c0);
             if (e != found) {
                 int off;
-                lds_barrier();  // the last expert's list has been used
-                cnt = s_find.find(a, e, &off);
+                if (found >= 0) lds_barrier();  // the last expert's list has been used
+                cnt = s_find.find(a, few, e, &off);
                 found = e;
                 if constexpr (LAYER) {
                     if (g0 == 0 && c0 == 0) s_find.write_routes(a, off, cnt);
@@ -756,23 +819,30 @@ __global__ __launch_bounds__(NW* kWave, W::kReadWaves) void expert_rows_read(con
     const int row0 = blockIdx.x * (RT * kTile);
     int e = 0, cnt = a.n;
     if (a.ids) {
-        s_find.begin(a);
-        if constexpr (LAYER) s_find.write_slots(a.table);
-        // the blockIdx.y-th slot
-        int slot = blockIdx.y;
-        if (slot >= s_find.slots) return;
-        for (int e0 = 0;; e0 += kWave) {
-            const uint64_t m = __ballot(s_find.routes[e0 + lane_id()] > 0);
-            const int here = __popcll(m);
-            if (slot < here) {
-                const bool hit = ((m >> lane_id()) & 1) && count_below(m) == slot;
-                e = e0 + (int)__builtin_ctzll(__ballot(hit));
-                break;
+        FewRoutes few = {};
+        s_find.begin(a, few);
+        int slot = blockIdx.y;  // the slot-th expert reached
+        if (a.n <= kWave) {
+            uint64_t firsts = __ballot(few.first == lane_id());
+            if (slot >= __popcll(firsts)) return;
+            for (; slot > 0; --slot) firsts &= firsts - 1;
+            e = __builtin_amdgcn_readlane(few.id, (int)__builtin_ctzll(firsts));
+        } else {
+            if constexpr (LAYER) s_find.write_slots(a.table);
+            if (slot >= s_find.slots) return;
+            for (int e0 = 0;; e0 += kWave) {
+                const uint64_t m = __ballot(s_find.routes[e0 + lane_id()] > 0);
+                const int here = __popcll(m);
+                if (slot < here) {
+                    const bool hit = ((m >> lane_id()) & 1) && count_below(m) == slot;
+                    e = e0 + (int)__builtin_ctzll(__ballot(hit));
+                    break;
+                }
+                slot -= here;
             }
-            slot -= here;
         }
         int off;
-        cnt = s_find.find(a, e, &off);
+        cnt = s_find.find(a, few, e, &off);
         if constexpr (LAYER) {
             if (blockIdx.x == 0) s_find.write_routes(a, off, cnt);
         }
@@ -793,7 +863,10 @@ __global__ __launch_bounds__(NW* kWave, W::kReadWaves) void expert_rows_read(con
 
 struct DownArgs {
     const u32x4* h;
-    const Table* table;
+    const Table* table;   // read where n > 64, otherwise:
+    const int* ids;       // [T*K]
+    const uint8_t* mask;  // [T*K] or NULL
+    int first;
     const float* scores;  // [T*K]
     int T, K, n, E;
     Weights w;            // [E, H, I]
@@ -801,11 +874,12 @@ struct DownArgs {
     float* out_f32;
 };
 
-// A job: up to two column blocks of one expert's routes.
+// A job: up to two column blocks of one expert's routes, from place `off` in
+// the list on. Packed, as the second kernel keeps up to 2048 of them in LDS.
 struct Job {
-    uint16_t expert, cnt;
-    int off;
+    uint32_t expert : 12, cnt : 8, off : 12;
 };
+static_assert(kMaxExperts < (1 << 12) && kMaxRoutes <= (1 << 12), "fields of Job");
 
 // One work-group: RT 8-row tiles of the output for all tokens, its waves
 // splitting the (job, chunk) steps of all experts reached in equal, unbroken
@@ -829,31 +903,50 @@ __global__ __launch_bounds__(NW* kWave, 2) void expert_down(const DownArgs a) {
     const int row0 = blockIdx.x * (RT * kTile);
 
     for (int i = tid; i < NW * a.T * R4; i += NW * kWave) s_sum[i] = f32x4{0, 0, 0, 0};
-    const int n_slots = a.table->n_slots;
-    const int live = n_slots ? a.table->offset[n_slots] : 0;
-    for (int i = tid; i < live; i += NW * kWave) {
-        const int r = a.table->route[i];
-        s_route[i] = (uint16_t)r;
-        s_score[i] = a.scores[r];
-        s_token[i] = (uint8_t)(r / a.K);
-    }
-    if (wave == 0) {
-        int jobs = 0;
-        for (int s0 = 0; s0 < n_slots; s0 += kWave) {
-            const int s = s0 + lane;
-            const bool in = s < n_slots;
-            const int e = in ? a.table->expert[s] : 0;
-            const int off = in ? a.table->offset[s] : 0;
-            const int cnt = in ? a.table->offset[s + 1] - off : 0;
-            const int mine = (cnt + 2 * kRoutes - 1) / (2 * kRoutes);
-            const int inc = wave_inclusive_sum(mine);
-            for (int j = 0; j < mine; ++j)
-                s_job[jobs + inc - mine + j] = {(uint16_t)e,
-                                                (uint16_t)min(2 * kRoutes, cnt - j * 2 * kRoutes),
-                                                off + j * 2 * kRoutes};
-            jobs += __builtin_amdgcn_readlane(inc, kWave - 1);
+    if (a.n <= kWave) {
+        // each wave writes the same tables
+        const FewRoutes few = FewRoutes::read(a.ids, a.mask, a.n, a.first, a.E);
+        const float score = a.scores[min(lane, a.n - 1)];
+        const int at = few.place();
+        if (few.id >= 0) {
+            s_route[at] = (uint16_t)lane;
+            s_score[at] = score;
+            s_token[at] = (uint8_t)(lane / a.K);
         }
-        if (lane == 0) s_jobs = jobs;
+        const int mine = few.jobs(2 * kRoutes), to = wave_inclusive_sum(mine);
+        for (int j = 0; j < mine; ++j)
+            s_job[to - mine + j] = {
+                (uint32_t)few.id,
+                (uint32_t)min(2 * kRoutes, __popcll(few.peers) - j * 2 * kRoutes),
+                (uint32_t)(at + j * 2 * kRoutes)};
+        if (lane == kWave - 1) s_jobs = to;
+    } else {
+        const int n_slots = a.table->n_slots;
+        const int live = n_slots ? a.table->offset[n_slots] : 0;
+        for (int i = tid; i < live; i += NW * kWave) {
+            const int r = a.table->route[i];
+            s_route[i] = (uint16_t)r;
+            s_score[i] = a.scores[r];
+            s_token[i] = (uint8_t)(r / a.K);
+        }
+        if (wave == 0) {
+            int jobs = 0;
+            for (int s0 = 0; s0 < n_slots; s0 += kWave) {
+                const int s = s0 + lane;
+                const bool in = s < n_slots;
+                const int e = in ? a.table->expert[s] : 0;
+                const int off = in ? a.table->offset[s] : 0;
+                const int cnt = in ? a.table->offset[s + 1] - off : 0;
+                const int mine = (cnt + 2 * kRoutes - 1) / (2 * kRoutes);
+                const int to = jobs + wave_inclusive_sum(mine);
+                for (int j = 0; j < mine; ++j)
+                    s_job[to - mine + j] = {
+                        (uint32_t)e, (uint32_t)min(2 * kRoutes, cnt - j * 2 * kRoutes),
+                        (uint32_t)(off + j * 2 * kRoutes)};
+                jobs = __builtin_amdgcn_readlane(to, kWave - 1);
+            }
+            if (lane == 0) s_jobs = jobs;
+        }
     }
     lds_barrier();
 
@@ -866,12 +959,16 @@ __global__ __launch_bounds__(NW* kWave, 2) void expert_down(const DownArgs a) {
     const typename W::Lane l = W::lane_of(a.w, lane);
 
     if (lo < hi) {
-        // Weights are loaded a chunk ahead, inputs half a chunk (they come
-        // from the caches, and a whole chunk of two blocks twice would take
-        // half the registers).
-        constexpr int HS = W::kSteps / 2;
+        // Weights are loaded a chunk ahead. The inputs, which come from the
+        // caches, half a chunk ahead where a chunk is four steps: a whole one
+        // of two blocks, twice, would take half the registers. For bf16's two
+        // steps that is too late (186 us against 140 on a rank's 32 experts
+        // and 128 tokens), and the registers are there for a whole chunk.
+        constexpr bool kHalves = W::kSteps == 4;
+        constexpr int HS = kHalves ? W::kSteps / 2 : W::kSteps;
+        constexpr int HN = kHalves ? 2 : 1;
         typename W::Reg r[2][RT];
-        u32x4 x[2][2][HS];  // [half][block]
+        u32x4 x[2][2][HS];  // [half, or chunk][block]
         f32x4 acc[RT][2];
 #pragma unroll
         for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = f32x4{0, 0, 0, 0};
@@ -888,7 +985,7 @@ __global__ __launch_bounds__(NW* kWave, 2) void expert_down(const DownArgs a) {
             for (int i = 0; i < RT; ++i) wp[i] = W::at(a.w, e, row0 + i * kTile);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
-                xp[b].row(s_route[j.off + min(b * kRoutes + (lane & (kRoutes - 1)), cnt - 1)],
+                xp[b].row(s_route[(int)j.off + min(b * kRoutes + (lane & (kRoutes - 1)), cnt - 1)],
                           hv, lane);
             p.two = cnt > kRoutes;
         };
@@ -896,9 +993,9 @@ __global__ __launch_bounds__(NW* kWave, 2) void expert_down(const DownArgs a) {
 #pragma unroll
             for (int i = 0; i < RT; ++i) W::load(r[d][i], wp[i], l, p.chunk);
         };
-        auto load_x = [&](auto h, const At& p) MEP_INLINE {
-            xp[0].template load<true>(x[h][0], hb, p.chunk * 2 + h);
-            if (p.two) xp[1].template load<true>(x[h][1], hb, p.chunk * 2 + h);
+        auto load_x = [&](auto to, auto h, const At& p) MEP_INLINE {
+            xp[0].template load<true>(x[to][0], hb, p.chunk * HN + h);
+            if (p.two) xp[1].template load<true>(x[to][1], hb, p.chunk * HN + h);
         };
         auto fold = [&](int job) MEP_INLINE {  // adds a job's sums to its tokens'
             const Job j = s_job[job];
@@ -906,8 +1003,8 @@ __global__ __launch_bounds__(NW* kWave, 2) void expert_down(const DownArgs a) {
             any_of<2>([&](auto b) MEP_INLINE {
                 const int c = b * kRoutes + (lane & (kRoutes - 1));
                 bool todo = lane < 32 && (lane & 15) < kRoutes && c < cnt;
-                const int tok = s_token[j.off + min(c, cnt - 1)];
-                const float sc = s_score[j.off + min(c, cnt - 1)];
+                const int tok = s_token[(int)j.off + min(c, cnt - 1)];
+                const float sc = s_score[(int)j.off + min(c, cnt - 1)];
                 f32x4 v[RT];
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
@@ -937,21 +1034,25 @@ __global__ __launch_bounds__(NW* kWave, 2) void expert_down(const DownArgs a) {
         // Both blocks are always multiplied (the second's inputs are stale
         // where a job has one, and its sums not used): a branch here costs
         // more than the matrix cores' time.
-        auto use = [&](auto d, auto h) MEP_INLINE {
-            W::template mma<h * HS, HS, RT, 2>(r[d], x[h], acc);
+        auto use = [&](auto d, auto from, auto h) MEP_INLINE {
+            W::template mma<h * HS, HS, RT, 2>(r[d], x[from], acc);
         };
         constexpr std::integral_constant<int, 0> k0{};
         constexpr std::integral_constant<int, 1> k1{};
         At cur = {lo / KC, lo % KC, 0};
         open(cur);
         load_w(k0, cur);
-        load_x(k0, cur);
+        load_x(k0, k0, cur);
         int s = lo;
         while (!any_of<2>([&](auto d) MEP_INLINE {
-            load_x(k1, cur);
+            if constexpr (kHalves) load_x(k1, k1, cur);
             if (s + 1 >= hi) {
-                use(d, k0);
-                use(d, k1);
+                if constexpr (kHalves) {
+                    use(d, k0, k0);
+                    use(d, k1, k1);
+                } else {
+                    use(d, d, k0);
+                }
                 fold(cur.job);
                 return true;
             }
@@ -960,10 +1061,16 @@ __global__ __launch_bounds__(NW* kWave, 2) void expert_down(const DownArgs a) {
                 nxt = {cur.job + 1, 0, 0};
                 open(nxt);
             }
-            load_w(std::integral_constant<int, 1 - d>{}, nxt);
-            use(d, k0);
-            load_x(k0, nxt);
-            use(d, k1);
+            constexpr std::integral_constant<int, 1 - d> other{};
+            load_w(other, nxt);
+            if constexpr (kHalves) {
+                use(d, k0, k0);
+                load_x(k0, k0, nxt);
+                use(d, k1, k1);
+            } else {
+                load_x(other, k0, nxt);
+                use(d, d, k0);
+            }
             if (nxt.chunk == 0) fold(cur.job);
             cur = nxt;
             ++s;
@@ -1038,26 +1145,28 @@ void launch_rows(hipStream_t s, const RowsArgs& a) {
 }
 
 inline size_t down_lds(int nw, int rt, int T, int n) {
-    return (size_t)nw * T * rt * 2 * 16 + (size_t)n * (8 + 4 + 2 + 1) + 16;
+    return (size_t)nw * T * rt * 2 * 16 + (size_t)n * (4 + 4 + 2 + 1) + 16;
 }
 
-#ifndef DN_SRT
-#define DN_SRT 2
-#define DN_SNW 8
+#ifndef DN_ONE
+#define DN_ONE 512
 #endif
 template <class W, int TERMS, int RT, int NW>
 void launch_down(hipStream_t s, const DownArgs& d) {
-    hipLaunchKernelGGL((expert_down<W, TERMS, RT, NW>), dim3(tiles_of(d.w.N, RT)),
-                       dim3(NW * kWave), down_lds(NW, RT, d.T, d.n), s, d);
+    const size_t lds = down_lds(NW, RT, d.T, d.n);
+    auto kernel = expert_down<W, TERMS, RT, NW>;
+    hipLaunchKernelGGL(kernel, dim3(tiles_of(d.w.N, RT)), dim3(NW * kWave), lds, s, d);
 }
 
 template <class W, int TERMS>
 void launch_down(hipStream_t s, const DownArgs& d) {
     if constexpr (W::kWide) {
-        if (d.T <= 32 && tiles_of(d.w.N, 4) >= kCus * 3 / 4) return launch_down<W, TERMS, 4, 8>(s, d);
+        if (tiles_of(d.w.N, 4) >= kCus * 3 / 4)
+            return d.T <= 32 ? launch_down<W, TERMS, 4, 8>(s, d) : launch_down<W, TERMS, 4, 4>(s, d);
     }
-    if (d.T <= 64) return launch_down<W, TERMS, DN_SRT, DN_SNW>(s, d);
-    launch_down<W, TERMS, 2, 4>(s, d);
+    if (d.T > 64) return launch_down<W, TERMS, 2, 4>(s, d);
+    if (tiles_of(d.w.N, 1) > DN_ONE) return launch_down<W, TERMS, 2, 8>(s, d);
+    launch_down<W, TERMS, 1, 8>(s, d);
 }
 
 template <class W>

@@ -128,6 +128,9 @@ extern "C" int mep_moe_layer(int T, int K, int H, int I, int first, const uint16
     DownArgs d = {};
     d.h = a.h;
     d.table = a.table;
+    d.ids = a.ids;
+    d.mask = mask;
+    d.first = first;
     d.scores = scores;
     d.T = T;
     d.K = K;

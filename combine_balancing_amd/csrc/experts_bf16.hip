@@ -5,7 +5,10 @@ namespace mep {
 namespace experts {
 
 void layer_bf16(hipStream_t s, const RowsArgs& a, const DownArgs& d) {
-    launch_layer<Bf16Weights>(s, a, d);
+    if (a.w.K % 128 == 0 && d.w.K % 128 == 0)
+        launch_layer<Bf16Weights<true>>(s, a, d);
+    else
+        launch_layer<Bf16Weights<false>>(s, a, d);
 }
 
 }  // namespace experts
