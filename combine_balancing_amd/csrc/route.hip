@@ -136,6 +136,10 @@ __device__ __forceinline__ double lanes_sum(double v) {
     return lanes_reduce<L>(v, [](double a, double b) { return a + b; });
 }
 
+// Logits in one load of a lane's V: 16 bytes where they divide V, else 4.
+template <typename LT, int V>
+constexpr int kLaneVec = V % (16 / (int)sizeof(LT)) == 0 ? 16 / (int)sizeof(LT) : 4;
+
 constexpr double kNone = -1e300;  // an expert that cannot be taken (c is above -1e39)
 
 // L lanes per token; lane i of them holds experts i * V .. i * V + V - 1.
@@ -161,8 +165,8 @@ __global__ __launch_bounds__(kRouteThreads) void route_lanes(
     const LT* row = logits + (size_t)t * E;
 
     float l[V];
-    if (wide) {  // rows and lanes start on 16 bytes, E is a multiple of V
-        constexpr int N = 16 / sizeof(LT), M = V < N ? V : N;
+    if (wide) {  // rows and lanes start on whole vectors, E is a multiple of V
+        constexpr int M = kLaneVec<LT, V>;
         typedef LT vec __attribute__((ext_vector_type(M)));
 #pragma unroll
         for (int v = 0; v < V; v += M) {
@@ -486,7 +490,8 @@ template <typename LT, int L, int V>
 bool try_lanes(hipStream_t s, bool sig, const void* logits, const float* bias, int ng, int tg,
                int renorm, float scale, int* ids, float* scores, int T, int E, int K) {
     if (E > L * V || K > L || (ng > 1 && (E / ng) % V != 0)) return false;
-    constexpr size_t kVec = V * sizeof(LT) < 16 ? V * sizeof(LT) : 16;
+    static_assert(V % kLaneVec<LT, V> == 0, "whole vectors per lane");
+    constexpr size_t kVec = kLaneVec<LT, V> * sizeof(LT);
     const int wide = E % V == 0 && (E * sizeof(LT)) % kVec == 0 && (uintptr_t)logits % kVec == 0;
     constexpr int kTokens = kRouteThreads / L;
     hipLaunchKernelGGL((route_lanes<LT, L, V>), dim3((T + kTokens - 1) / kTokens),

@@ -460,3 +460,127 @@ def test_no_tokens():
     out, _ = cba.moe_layer(torch.empty(0, 8, dtype=torch.bfloat16, device="cuda"), i32,
                            torch.empty(0, 2, device="cuda"), w13, w2)
     assert out.shape == (0, 8)
+
+
+# ------------------------------------------------- sizes of the wide variants
+#
+# The references below run in float64 on the GPU (two-dimensional products),
+# with the same bounds as expert_ref.
+
+
+def _q4_gpu(g, E, N, K, kind, group, zeros, dt, exact):
+    import torch
+
+    import combine_balancing_amd as cba
+    G = -(-K // group)
+    codes = torch.randint(0, 16, (E, N, K), generator=g, device="cuda", dtype=torch.uint8)
+    if exact:
+        s = torch.exp2(torch.randint(-3, 3, (E, N, G), generator=g, device="cuda").float())
+    else:
+        s = (torch.rand(E, N, G, generator=g, device="cuda") + 0.2) / K ** 0.5 / 4
+    s = s.to(dt)
+    z = None
+    if zeros:
+        z = torch.randint(0, 16, (E, N, G), generator=g, device="cuda", dtype=torch.uint8)
+    w = cba.q4_pack(codes, s, zeros=z, group=group, kind=kind)
+    table = torch.tensor(ref.FP4, device="cuda")
+
+    def dense(e):
+        sv = s[e].double().repeat_interleave(group, 1)[:, :K]
+        if kind == "fp4":
+            v = table[codes[e].long()] * sv
+            return v, v.abs()
+        zv = 8.0 if z is None else z[e].double().repeat_interleave(group, 1)[:, :K]
+        return (codes[e].double() - zv) * sv, 290.0 * sv
+    return w, dense
+
+
+@pytest.mark.parametrize("kind,group,zeros,scale", KINDS)
+@pytest.mark.parametrize("T,R,E,N,K", [(8, 8, 32, 520, 264),      # 64 routes, one chunk a wave
+                                       (20, 8, 40, 417, 264),     # more than 64 routes
+                                       (40, 2, 16, 1048, 4360),   # two chunks a wave
+                                       (3, 1, 3, 7000, 2056), (9, 4, 4, 600, 1000),
+                                       (130, 3, 3, 90, 520), (2, 0, 1, 16500, 264)])
+def test_matvec_wide_exact(kind, group, zeros, scale, T, R, E, N, K):
+    # whole numbers and power-of-two scales: all partial sums are exact
+    torch = require_gpu()
+    import combine_balancing_amd as cba
+    note(f"matvec wide {kind} g={group} z={zeros} {(T, R, E, N, K)}")
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    dt = torch.bfloat16 if scale == "bf16" else torch.float16
+    w, dense = _q4_gpu(g, E, N, K, kind, group, zeros, dt, True)
+    x = torch.randint(-3, 4, (T, K), generator=g, device="cuda").bfloat16()
+    if R == 0:
+        got = cba.expert_matvec_q4(x, w, out_dtype=torch.float32)
+        torch.cuda.synchronize()
+        assert torch.equal(got.double(), x.double() @ dense(0)[0].t())
+        return
+    ids = torch.randint(-1, E, (T, R), generator=g, device="cuda", dtype=torch.int32)
+    ids[::3] = ids[0, 0].clamp(0)  # one crowded expert
+    got = cba.expert_matvec_q4(x, w, ids=ids, out=torch.full((T, R, N), 5.0, device="cuda"))
+    torch.cuda.synchronize()
+    want = torch.full((T, R, N), 5.0, device="cuda", dtype=torch.float64)
+    for e in range(E):
+        t, r = (ids == e).nonzero(as_tuple=True)
+        if t.numel():
+            want[t, r] = x[t].double() @ dense(e)[0].t()
+    assert torch.equal(got.double(), want)
+
+
+@pytest.mark.parametrize("kind,group,zeros,scale", [("bf16", 0, False, "bf16"),
+                                                    ("int4", 128, False, "bf16"),
+                                                    ("int4", 64, True, "fp16"),
+                                                    ("int4", 128, True, "bf16"),
+                                                    ("fp4", 32, False, "bf16"),
+                                                    ("fp4", 128, False, "fp16")])
+@pytest.mark.parametrize("T,K,E,H,I", [(16, 4, 64, 1032, 264),    # held, one chunk a wave
+                                       (33, 4, 64, 4104, 264),    # held, two; two tiles out
+                                       (5, 3, 64, 6152, 1032),    # held, four (bf16); four tiles
+                                       (40, 2, 24, 6152, 136),    # four tiles, four waves
+                                       (100, 4, 6, 4104, 136),    # read in pairs of blocks
+                                       (128, 8, 8, 6152, 264)])
+def test_layer_wide(kind, group, zeros, scale, T, K, E, H, I):
+    torch = require_gpu()
+    import combine_balancing_amd as cba
+    note(f"layer wide {kind} g={group} z={zeros} {(T, K, E, H, I)}")
+    g = torch.Generator(device="cuda").manual_seed(T + H + I)
+    dt = torch.bfloat16 if scale == "bf16" else torch.float16
+    first = 11
+    if kind == "bf16":
+        w13 = (torch.randn(E, 2 * I, H, generator=g, device="cuda") / H ** 0.5).bfloat16()
+        w2 = (torch.randn(E, H, I, generator=g, device="cuda") / I ** 0.5).bfloat16()
+        d13, d2 = (lambda e: (w13[e].double(),) * 2), (lambda e: (w2[e].double(),) * 2)
+    else:
+        w13, d13 = _q4_gpu(g, E, 2 * I, H, kind, group, zeros, dt, False)
+        w2, d2 = _q4_gpu(g, E, H, I, kind, group, zeros, dt, False)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    ids = torch.randint(-2, E, (T, K), generator=g, device="cuda", dtype=torch.int32)
+    ids[::5, 0] = 3
+    mask = (torch.rand(T, K, generator=g, device="cuda") < 0.9).to(torch.uint8)
+    sc = torch.randn(T, K, generator=g, device="cuda")
+    want = torch.zeros(T, H, device="cuda", dtype=torch.float64)
+    lim = torch.zeros_like(want)
+    for e in range(E):
+        t, k = ((ids == e) & (mask > 0)).nonzero(as_tuple=True)
+        if t.numel() == 0:
+            continue
+        (a, am), (b, bm) = d13(e), d2(e)
+        xt, s = x[t].double(), sc[t, k].double()[:, None]
+        gu, d = xt @ a.t(), ref.product_slack(xt.abs() @ am.abs().t(), H)
+        gate, up, dg, du = gu[:, :I], gu[:, I:], d[:, :I], d[:, I:]
+        sl = gate * torch.sigmoid(gate)
+        h = sl * up
+        dh = (1.1 * dg + 8 * ref.U32 * sl.abs()) * (up.abs() + du) + sl.abs() * du
+        dh = dh + h.abs() * 2.0 ** -16
+        y = h @ b.t()
+        ly = dh @ bm.abs().t() + ref.product_slack((h.abs() + dh) @ bm.abs().t(), I)
+        want.index_add_(0, t, s * y)
+        lim.index_add_(0, t, s.abs() * (ly + (4 + 17 * K) * ref.U32 * (y.abs() + ly)))
+    for f32 in (False, True):
+        ob, of = cba.moe_layer(x, ids + first, sc, w13, w2, first=first, mask=mask,
+                               out_bf16=not f32, out_f32=f32)
+        torch.cuda.synchronize()
+        got = of if f32 else ob
+        half = ref.HALF["fp32" if f32 else "bf16"]
+        err = (got.double() - want).abs()
+        assert bool((err <= lim + half * (want.abs() + lim)).all()), float((err - lim).max())

@@ -65,6 +65,53 @@ def test_route_sizes(dtype, T, E, K):
         _check(ld, l, K, scoring=scoring, bias=(0.2 * rng.standard_normal(E)).astype(np.float32))
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("E,ng,tg,K", [(16, 1, 1, 4), (48, 1, 1, 8), (52, 1, 1, 16), (64, 4, 2, 8),
+                                       (120, 1, 1, 8), (128, 8, 4, 8), (200, 1, 1, 6),
+                                       (256, 8, 4, 8), (255, 1, 1, 3), (256, 2, 1, 20),
+                                       (384, 1, 1, 8), (380, 1, 1, 8), (383, 1, 1, 5),
+                                       (384, 8, 3, 6), (500, 1, 1, 8), (512, 16, 4, 8),
+                                       (512, 1, 1, 33), (768, 1, 1, 8), (1000, 5, 2, 7),
+                                       (1024, 1, 1, 8)])
+def test_route_many_tokens(dtype, E, ng, tg, K):
+    """Enough tokens for the variants that put several on a wave, at widths
+    that fill their lanes, do not, or leave rows off the vector grid; checked
+    at every 13th token and the last."""
+    torch = require_gpu()
+    import combine_balancing_amd as cba
+    note(f"route many tokens {dtype} E={E} ng={ng} K={K}")
+    T = 4099
+    rng = np.random.default_rng(E + K)
+    ld, l = _logits(rng, T, E, dtype, masked=0.1 if E % 3 == 0 else 0.0)
+    rows = np.r_[np.arange(0, T, 13), T - 1]
+    for scoring, bias in (("softmax", None), ("sigmoid", 0.2)):
+        b = None if bias is None else (bias * rng.standard_normal(E)).astype(np.float32)
+        ids, sc = cba.route(ld, K, bias=None if b is None else torch.from_numpy(b).cuda(),
+                            scoring=scoring, n_group=ng, topk_group=tg)
+        torch.cuda.synchronize()
+        want_ids, want = ref.route(l[rows], K, bias=b, scoring=scoring, n_group=ng, topk_group=tg)
+        assert np.array_equal(ids.cpu().numpy()[rows], want_ids)
+        got = sc.cpu().numpy()[rows].astype(np.float64)
+        assert np.all(np.abs(got - want) <= SCORE_TOL * np.abs(want) + 2.0 ** -149)
+
+
+@pytest.mark.parametrize("offset", [1, 2, 4])
+def test_route_off_the_vector_grid(offset):
+    # logits that start inside a larger buffer, `offset` elements in
+    torch = require_gpu()
+    import combine_balancing_amd as cba
+    note(f"route offset {offset}")
+    rng = np.random.default_rng(offset)
+    for dtype in (torch.float32, torch.bfloat16):
+        for T, E in ((4100, 256), (7, 256), (4100, 384)):
+            buf = torch.from_numpy(rng.standard_normal(T * E + 8).astype(np.float32)).to(dtype).cuda()
+            l = buf[offset:offset + T * E].view(T, E)
+            a = cba.route(l, 8, scoring="sigmoid")
+            b = cba.route(l.clone(), 8, scoring="sigmoid")
+            torch.cuda.synchronize()
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,ng,tg,K", [(256, 8, 4, 8), (256, 8, 1, 32), (64, 64, 5, 5),
                                        (160, 8, 3, 6), (48, 3, 2, 4), (1024, 16, 4, 8),
