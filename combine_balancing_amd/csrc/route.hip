@@ -401,76 +401,103 @@ __global__ __launch_bounds__(kRouteThreads) void route_rows(
 //   sigmoid           dl[j] = g_j s_j (1 - s_j) at the chosen, 0 elsewhere
 //   softmax renorm    dl[j] = w_j (g_j - sum_i g_i w_i) at the chosen
 //   softmax           dl[e] = s_e ((chosen: g_e) - sum_i g_i s_i) everywhere
-template <typename LT, int V, bool SIGMOID>
-__global__ __launch_bounds__(kRouteThreads) void route_grad_rows(
+//
+// L lanes per token; lane j < K has the j-th chosen expert, and in the last
+// form each lane E / L experts. The row is put together in LDS, where the
+// chosen land by id, and leaves in 16-byte stores. Only the last form reads
+// whole rows; the others read the chosen logits, which still touches most
+// of a row's lines, so all are bound by reading and writing the rows once.
+// Several tokens a wave: one token a wave spent its life in the chain ids,
+// logits, sums (27.7 us for 32768 tokens of 256 experts, sigmoid, fp32).
+template <typename LT, int L>
+__global__ __launch_bounds__(kRouteThreads) void route_grad_lanes(
     const LT* __restrict__ logits, const int* __restrict__ ids, const float* __restrict__ dscores,
-    int renorm, float scale, LT* __restrict__ dlogits, int T, int E, int K) {
-    const int lane = lane_id();
-    const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x) / kWave;
-    const int t = blockIdx.x * kRouteWaves + w;
-    if (t >= T) return;
+    int sig, int renorm, float scale, LT* __restrict__ dlogits, int wide, int T, int E, int K) {
+    constexpr int kTokens = kRouteThreads / L;
+    extern __shared__ float s_rows[];  // [kTokens][pitch]
+    const int pitch = (E + 3) & ~3;
+    const int lane = lane_id(), i = lane & (L - 1), base = lane & ~(L - 1);
+    const int t_raw = blockIdx.x * kTokens + threadIdx.x / L;
+    const int t = min(t_raw, T - 1);  // lanes past T work on a real row, store nothing
     const LT* row = logits + (size_t)t * E;
-    int id = lane < K ? ids[(size_t)t * K + lane] : -1;
-    if ((unsigned)id >= (unsigned)E) id = -1;
-    const float lj = id >= 0 ? clean(widen(row[id])) : -INFINITY;
-    const bool live = lj > -INFINITY;
-    double g = live ? (double)dscores[(size_t)t * K + lane] * (double)scale : 0.0;
+    float* out = s_rows + (threadIdx.x / L) * pitch;
 
-    float l[V];
-    double top = 0.0, z = 1.0, dot = 0.0, dl = 0.0;
-    const bool dense = !SIGMOID && !renorm;
+    int id = i < K ? ids[(size_t)t * K + i] : -1;
+    double g = i < K ? (double)dscores[(size_t)t * K + i] * (double)scale : 0.0;
+    if ((unsigned)id >= (unsigned)E) id = -1;
+    const float lj = id >= 0 ? clean(widen<LT>(row[id])) : -INFINITY;
+    const bool live = lj > -INFINITY;
+    if (!live) g = 0.0;
+    const bool dense = !sig && !renorm;
+
+    double dl;  // of the chosen
     if (dense) {
         float m = -INFINITY;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = v * kWave + lane;
-            l[v] = e < E ? clean(widen(row[min(e, E - 1)])) : -INFINITY;
-            m = fmaxf(m, l[v]);
+        for (int e = i; e < E; e += L) m = fmaxf(m, clean(widen<LT>(row[e])));
+        const double top = lanes_max<L>(m);
+        double z = 0.0;
+        for (int e = i; e < E; e += L) {
+            const float l = clean(widen<LT>(row[e]));
+            z += l > -INFINITY ? exp_neg((double)l - top) : 0.0;
         }
-        top = wave_max_d(m);
-        double part = 0.0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) part += l[v] > -INFINITY ? exp((double)l[v] - top) : 0.0;
-        z = wave_sum_d(part);
-        const double s = live ? exp((double)lj - top) / z : 0.0;
-        dot = wave_sum_d(g * s);
-        dl = s * g;
-    } else if (SIGMOID) {
-        const double x = live ? exp(-fabs((double)lj)) : 0.0;  // s(1-s) = x / (1+x)^2
-        const double s = live ? (lj >= 0.0f ? 1.0 : x) / (1.0 + x) : 0.0;
-        const double ds = x / ((1.0 + x) * (1.0 + x));
-        if (renorm) {
-            const double d = wave_sum_d(s) + kRenormEps;
-            const double gw = wave_sum_d(g * (s / d));
-            g = (g - gw) / d;
+        z = lanes_sum<L>(z);
+        const double r = z > 0.0 ? 1.0 / z : 0.0;
+        const double s = live ? exp_neg((double)lj - top) * r : 0.0;
+        const double dot = lanes_sum<L>(g * s);
+        dl = s * (g - dot);
+        double twice = 0.0;  // an id given again adds its g
+        for (int k = 0; k < K; ++k) {
+            const double o = __shfl(g, base + k, kWave);
+            if (__shfl(id, base + k, kWave) == id) twice += o;
         }
-        dl = live ? g * ds : 0.0;
+        dl = s * (twice - dot);
+        for (int e = i; e < E; e += L) {
+            const float l = clean(widen<LT>(row[e]));
+            out[e] = l > -INFINITY ? (float)(-dot * (exp_neg((double)l - top) * r)) : 0.0f;
+        }
     } else {
-        const double m = wave_max_d(live ? (double)lj : -INFINITY);
-        const double x = live ? exp((double)lj - m) : 0.0;
-        const double d = wave_sum_d(x);
-        const double wj = d > 0.0 ? x / d : 0.0;
-        const double gw = wave_sum_d(g * wj);
-        dl = wj * (g - gw);
+        if (sig) {
+            const double x = live ? exp_neg(-fabs((double)lj)) : 0.0;  // s(1-s) = x / (1+x)^2
+            const double y = reciprocal(1.0 + x);
+            const double s = live ? (lj >= 0.0f ? y : x * y) : 0.0;
+            if (renorm) {
+                const double d = lanes_sum<L>(s) + kRenormEps;
+                g = (g - lanes_sum<L>(g * (s / d))) / d;
+            }
+            dl = live ? g * (x * y * y) : 0.0;
+        } else {
+            const double m = lanes_max<L>(live ? (double)lj : kNone);
+            const double x = live ? exp_neg((double)lj - m) : 0.0;
+            const double d = lanes_sum<L>(x);
+            const double w = d > 0.0 ? x / d : 0.0;
+            dl = w * (g - lanes_sum<L>(g * w));
+        }
+        double all = 0.0;  // in k order: an id given again adds up
+        for (int k = 0; k < K; ++k) {
+            const double o = __shfl(dl, base + k, kWave);
+            if (__shfl(id, base + k, kWave) == id) all += o;
+        }
+        dl = all;
+        for (int e = i * 4; e < pitch; e += L * 4)
+            *(rows::f32x4*)(out + e) = rows::f32x4{0, 0, 0, 0};
     }
-
-    double out[V];
+    // a token's lanes lie in one wave, whose LDS operations stay in order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (live) out[id] = (float)dl;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (t_raw >= T) return;
+    LT* dst = dlogits + (size_t)t * E;
+    if (wide) {
+        constexpr int N = 16 / sizeof(LT);
+        typedef LT vec __attribute__((ext_vector_type(N)));
+        for (int e = i * N; e < E; e += L * N) {
+            vec v;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        out[v] = 0.0;
-        if (dense && l[v] > -INFINITY) out[v] = -dot * (exp((double)l[v] - top) / z);
-    }
-    for (int k = 0; k < K; ++k) {  // in k order: an id given twice adds up
-        const int at = __shfl(id, k, kWave);
-        const double d = __shfl(dl, k, kWave);
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (at == v * kWave + lane) out[v] += d;
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = v * kWave + lane;
-        if (e < E) dlogits[(size_t)t * E + e] = narrow<LT>((float)out[v]);
+            for (int k = 0; k < N; ++k) v[k] = narrow<LT>(out[e + k]);
+            __builtin_nontemporal_store(v, (vec*)(dst + e));
+        }
+    } else {
+        for (int e = i; e < E; e += L) dst[e] = narrow<LT>(out[e]);
     }
 }
 
@@ -526,27 +553,26 @@ void dispatch_route(hipStream_t s, bool sig, const void* logits, const float* bi
         launch_route<LT, 16>(s, sig, logits, bias, ng, tg, renorm, scale, ids, scores, T, E, K);
 }
 
-template <typename LT, int V>
+template <typename LT, int L>
 void launch_route_grad(hipStream_t s, bool sig, const void* logits, const int* ids,
                        const float* ds, int renorm, float scale, void* dl, int T, int E, int K) {
-    const dim3 g((T + kRouteWaves - 1) / kRouteWaves), b(kRouteThreads);
-    if (sig)
-        hipLaunchKernelGGL((route_grad_rows<LT, V, true>), g, b, 0, s, (const LT*)logits, ids, ds,
-                           renorm, scale, (LT*)dl, T, E, K);
-    else
-        hipLaunchKernelGGL((route_grad_rows<LT, V, false>), g, b, 0, s, (const LT*)logits, ids, ds,
-                           renorm, scale, (LT*)dl, T, E, K);
+    constexpr int kTokens = kRouteThreads / L;
+    const int wide = (E * sizeof(LT)) % 16 == 0 && (uintptr_t)dl % 16 == 0;
+    hipLaunchKernelGGL((route_grad_lanes<LT, L>), dim3((T + kTokens - 1) / kTokens),
+                       dim3(kRouteThreads), (size_t)kTokens * ((E + 3) & ~3) * 4, s,
+                       (const LT*)logits, ids, ds, sig ? 1 : 0, renorm, scale, (LT*)dl, wide, T, E,
+                       K);
 }
 
+// Whole waves for few tokens (a token's chain of steps is shorter), for many
+// chosen, and for rows of which 16 tokens would not fit a work-group's LDS.
 template <typename LT>
 void dispatch_route_grad(hipStream_t s, bool sig, const void* logits, const int* ids,
                          const float* ds, int renorm, float scale, void* dl, int T, int E, int K) {
-    if (E <= 256)
-        launch_route_grad<LT, 4>(s, sig, logits, ids, ds, renorm, scale, dl, T, E, K);
-    else if (E <= 512)
-        launch_route_grad<LT, 8>(s, sig, logits, ids, ds, renorm, scale, dl, T, E, K);
-    else
+    if (T >= kRouteManyTokens && K <= 16 && E <= 512)
         launch_route_grad<LT, 16>(s, sig, logits, ids, ds, renorm, scale, dl, T, E, K);
+    else
+        launch_route_grad<LT, 64>(s, sig, logits, ids, ds, renorm, scale, dl, T, E, K);
 }
 
 bool known_dtype(int d) {

@@ -214,6 +214,31 @@ def test_route_grad_sizes(dtype, T, E, K):
             _grad_check(ld, l, ids, d, dtype, scoring=scoring, renormalize=renorm, scale=2.5)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("E,K", [(16, 4), (131, 8), (256, 8), (384, 16), (512, 2), (600, 8),
+                                 (256, 20)])
+def test_route_grad_many_tokens(dtype, E, K):
+    torch = require_gpu()
+    import combine_balancing_amd as cba
+    note(f"route_grad many tokens {dtype} E={E} K={K}")
+    T = 4099
+    rng = np.random.default_rng(E * K)
+    ld, l = _logits(rng, T, E, dtype, masked=0.1 if E % 2 else 0.0)
+    d = rng.standard_normal((T, K)).astype(np.float32)
+    rows = np.r_[np.arange(0, T, 13), T - 1]
+    for scoring in ("softmax", "sigmoid"):
+        ids, _ = cba.route(ld, K, scoring=scoring)
+        ids[26] = ids[26, 0].item()         # one id K times
+        for renorm in (True, False):
+            got = cba.route_grad(ld, ids, torch.from_numpy(d).cuda(), scoring=scoring,
+                                 renormalize=renorm, scale=2.5)
+            torch.cuda.synchronize()
+            want = ref.route_grad(l[rows], ids.cpu().numpy()[rows], d[rows], scoring, renorm, 2.5)
+            got = got.double().cpu().numpy()[rows]
+            slack = 2.0 ** -46 * np.abs(d).max() * 2.5 * K * 1e3
+            assert np.all(np.abs(got - want) <= GRAD_TOL[dtype] * np.abs(want) + TINY[dtype] + slack)
+
+
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_route_grad_masked_repeated_and_bad_ids(scoring, renorm):
