@@ -2,7 +2,8 @@
 
 The work is done by libmep.so (C ABI in include/mep.h, HIP kernels under
 csrc/). This package is its binding: ``_binding`` holds the raw entry points
-under their C names, ``api`` the tensor-level calls. Importing the package
+under their C names, ``api`` the tensor-level calls of the exchange and
+``experts`` those of the router and the experts themselves. Importing the package
 does not load the library; the first call does, and raises if it has not
 been built (``python -m combine_balancing_amd.build``).
 """

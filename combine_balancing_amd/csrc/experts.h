@@ -116,9 +116,8 @@ __device__ __forceinline__ int lane_vec(int lane) { return (lane >> 4) + ((lane 
 template <bool WHOLE>
 struct Bf16Weights {
     static constexpr int kSteps = 2;
-    static constexpr int kMaxHeld = 4;    // chunks of inputs that a wave can hold
-    static constexpr int kReadWaves = 2;  // waves per SIMD that expert_rows_read is built for
-    static constexpr bool kWide = true;   // whether expert_down takes four tiles at a time
+    static constexpr int kMaxHeld = 4;   // chunks of inputs that a wave can hold
+    static constexpr bool kWide = true;  // whether expert_down takes four tiles at a time
     struct Reg {
         u32x4 a[kSteps];
     };
@@ -164,21 +163,23 @@ struct Bf16Weights {
 // accumulators' lanes need them (groups of 32: those of the steps' first
 // halves, then those of the second, since lanes q >= 2 hold the latter).
 //
-// An int4 code q becomes the bf16 number 128 + q by or-ing it into the
-// mantissa of 128 (one shift and one and-or per two codes). The constant is
-// taken out of the sum again by a product of the same inputs with a constant
-// row, -(128 + 8) for symmetric codes, whose result is the accumulator that
-// the code product starts from: sum (128 + q) x - sum 136 x = sum (q - 8) x.
-// With zero points the constant row is -128 and z of the row times
-// sum x = -1/128 of that result is subtracted per row. All terms are exact
-// products summed in fp32; the offset makes them at most 27 times larger
-// than the terms of the result, which costs under five of fp32's 24 bits.
+// An int4 code q becomes the bf16 number 16 + q by or-ing it into the upper
+// mantissa bits of 16 (a shift, and an and-or, per two codes). The constant
+// is taken out of the sum again by a product of the same inputs with a
+// constant row, -(16 + 8) for symmetric codes, whose result is the
+// accumulator that the code product starts from:
+// sum (16 + q) x - sum 24 x = sum (q - 8) x. With zero points the constant
+// row is -16 and z of the row times sum x = -1/16 of that result is
+// subtracted per row. All terms are exact products summed in fp32; 16 is the
+// smallest power of two that keeps all sixteen codes in one binade, so the
+// terms are at most 7 times larger than the result's. (With the code in the
+// lowest mantissa bits the constant is 128: an fp32 output was 1.3e-6 from
+// the exact one where 3e-7 is fp32's share.)
 // A 4-bit float is converted by the hardware, two codes per instruction.
 template <bool FP4, int G, bool ZP, bool F16>
 struct PackedWeights {
     static constexpr int kSteps = 4;
     static constexpr int kMaxHeld = 2;
-    static constexpr int kReadWaves = 2;
     static constexpr bool kWide = G == 128;
     static constexpr int SM = G == 128 ? 2 : 1;  // steps per scale
     static constexpr int GL = kSteps / SM;       // scales per lane, row and chunk
@@ -229,15 +230,15 @@ struct PackedWeights {
         }
         return __uint_as_float(hi ? w & 0xffff0000u : w << 16);
     }
-    // k128: 128.0 twice. Given in a vector register, so that the mask (a
+    // k16: 16.0 twice. Given in a vector register, so that the mask (a
     // scalar) and it fit one v_and_or_b32; as two constants they took two
     // instructions.
     static __device__ __forceinline__ uint32_t offset_bits() {
-        uint32_t k128 = 0x43004300u;
-        asm("" : "+v"(k128));
-        return k128;
+        uint32_t k16 = 0x41804180u;
+        asm("" : "+v"(k16));
+        return k16;
     }
-    static __device__ __forceinline__ u32x4 decode(uint32_t d, uint32_t k128) {
+    static __device__ __forceinline__ u32x4 decode(uint32_t d, uint32_t k16) {
         u32x4 o;
         if constexpr (FP4) {
             o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 0));
@@ -245,8 +246,10 @@ struct PackedWeights {
             o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 2));
             o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, 1.0f, 3));
         } else {
-#pragma unroll
-            for (int p = 0; p < 4; ++p) o[p] = ((d >> (4 * p)) & 0x000f000fu) | k128;
+            o[0] = (d & 0x00780078u) | k16;
+            o[1] = ((d >> 4) & 0x00780078u) | k16;
+            o[2] = ((d >> 8) & 0x00780078u) | k16;
+            o[3] = (__builtin_amdgcn_alignbit(d, d, 12) & 0x00780078u) | k16;
         }
         return o;
     }
@@ -254,9 +257,9 @@ struct PackedWeights {
     static __device__ __forceinline__ void mma(const Reg (&r)[NT], const u32x4 (&x)[NB][SN],
                                                f32x4 (&acc)[NT][NB]) {
         static_assert(S0 % SM == 0 && SN % SM == 0, "whole groups");
-        constexpr uint32_t kOff = ZP ? 0xc300c300u : 0xc308c308u;  // -128, -136
+        constexpr uint32_t kOff = ZP ? 0xc180c180u : 0xc1c0c1c0u;  // -16, -24
         const u32x4 off = {kOff, kOff, kOff, kOff};
-        const uint32_t k128 = offset_bits();
+        const uint32_t k16 = offset_bits();
 #pragma unroll
         for (int g = S0 / SM; g < (S0 + SN) / SM; ++g) {
             f32x4 x0[NB];
@@ -275,7 +278,7 @@ struct PackedWeights {
                 for (int b = 0; b < NB; ++b) c[b] = x0[b];
 #pragma unroll
                 for (int j = 0; j < SM; ++j) {
-                    const u32x4 a = decode(r[i].a[g * SM + j], k128);
+                    const u32x4 a = decode(r[i].a[g * SM + j], k16);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) c[b] = mfma(a, x[b][g * SM + j - S0], c[b]);
                 }
@@ -286,7 +289,7 @@ struct PackedWeights {
                     for (int b = 0; b < NB; ++b) {
                         float v = c[b][k];
                         if constexpr (ZP) {
-                            const float z = (float)((r[i].z[g] >> (8 * k)) & 0xffu) * (1.0f / 128);
+                            const float z = (float)((r[i].z[g] >> (8 * k)) & 0xffu) * (1.0f / 16);
                             v = __builtin_fmaf(z, x0[b][k], v);
                         }
                         acc[i][b][k] = __builtin_fmaf(s, v, acc[i][b][k]);
@@ -813,7 +816,7 @@ __device__ __forceinline__ void rows_pass(const RowsArgs& a, const Finder& find,
 }
 
 template <class W, bool LAYER, int RT, int NW>
-__global__ __launch_bounds__(NW* kWave, W::kReadWaves) void expert_rows_read(const RowsArgs a) {
+__global__ __launch_bounds__(NW* kWave, 2) void expert_rows_read(const RowsArgs a) {
     __shared__ Finder s_find;
     __shared__ f32x4 s_part[NW * (LAYER ? 2 : 1) * RT * 2 * 32];
     const int row0 = blockIdx.x * (RT * kTile);
@@ -1102,17 +1105,8 @@ constexpr int kCus = 256;
 
 inline int tiles_of(int rows, int rt) { return (rows + rt * kTile - 1) / (rt * kTile); }
 
-#ifndef HELD_MIN
-#define HELD_MIN 2048
-#endif
-#ifndef HELD_NT1
-#define HELD_NT1 4
-#define HELD_NT2 2
-#endif
-#ifndef READ_RT
-#define READ_RT 2
-#define READ_NW 4
-#endif
+// Tiles over all experts from which on expert_rows_held is used.
+constexpr long long kHeldTiles = 2048;
 
 template <class W, bool LAYER, int NT, int XC>
 void launch_held(hipStream_t s, const RowsArgs& a, int kc) {
@@ -1125,21 +1119,32 @@ void launch_held(hipStream_t s, const RowsArgs& a, int kc) {
                        dim3(nw * kWave), (size_t)2 * nw * NT * 32 * 16, s, a, groups);
 }
 
+// Which of the two first kernels runs. Held inputs pay where an expert gets
+// few routes (they are multiplied 8 at a time, and more routes read the
+// weights again) and every CU has several row groups to go through: 28 fp4
+// experts of 7168x2048 with 4-5 routes each take 53 us held against 103 read
+// along, 64 int4 experts of 4096x7168 186 against 203. One expert's 5 rows of
+// 1001x2504 take 13.1 held and 10.2 read, and at 8 routes an expert and more
+// (32 experts, 128 tokens, most of them other ranks') reading along in pairs
+// of blocks is at 7.1 TB/s. Inputs beyond what 16 waves hold are read too.
+// Two tiles in flight where a wave holds two chunks or more (four spill),
+// four where it holds one (60 us against 67 on the fp4 products).
 template <class W, bool LAYER>
 void launch_rows(hipStream_t s, const RowsArgs& a) {
     const int kc = chunks<W>(a.w.K);
     const int slots = a.ids ? (a.n < a.E ? a.n : a.E) : 1;
     const int rows = LAYER ? a.I : a.w.N;
-    if (a.n <= kCols * slots && kc <= W::kMaxHeld * kMaxWaves && (long long)slots * tiles_of(rows, 1) >= HELD_MIN) {
+    if (a.n <= kCols * slots && kc <= W::kMaxHeld * kMaxWaves &&
+        (long long)slots * tiles_of(rows, 1) >= kHeldTiles) {
         if (kc <= kMaxWaves)
-            launch_held<W, LAYER, HELD_NT1, 1>(s, a, kc);
+            launch_held<W, LAYER, 4, 1>(s, a, kc);
         else if (kc <= 2 * kMaxWaves)
-            launch_held<W, LAYER, HELD_NT2, 2>(s, a, kc);
+            launch_held<W, LAYER, 2, 2>(s, a, kc);
         else if constexpr (W::kMaxHeld == 4)
             launch_held<W, LAYER, 2, 4>(s, a, kc);
         return;
     }
-    constexpr int RT = READ_RT, NW = READ_NW;
+    constexpr int RT = 2, NW = 4;
     hipLaunchKernelGGL((expert_rows_read<W, LAYER, RT, NW>), dim3(tiles_of(rows, RT), slots),
                        dim3(NW * kWave), 0, s, a);
 }
@@ -1148,16 +1153,20 @@ inline size_t down_lds(int nw, int rt, int T, int n) {
     return (size_t)nw * T * rt * 2 * 16 + (size_t)n * (4 + 4 + 2 + 1) + 16;
 }
 
-#ifndef DN_ONE
-#define DN_ONE 512
-#endif
 template <class W, int TERMS, int RT, int NW>
 void launch_down(hipStream_t s, const DownArgs& d) {
-    const size_t lds = down_lds(NW, RT, d.T, d.n);
-    auto kernel = expert_down<W, TERMS, RT, NW>;
-    hipLaunchKernelGGL(kernel, dim3(tiles_of(d.w.N, RT)), dim3(NW * kWave), lds, s, d);
+    hipLaunchKernelGGL((expert_down<W, TERMS, RT, NW>), dim3(tiles_of(d.w.N, RT)),
+                       dim3(NW * kWave), down_lds(NW, RT, d.T, d.n), s, d);
 }
 
+// Four tiles a work-group where that still gives three work-groups to four
+// CUs: the inputs, read once per work-group, are then a smaller part of what
+// moves (64 int4 experts, 32 tokens: 142 us against 176 with two tiles; a
+// rank's 32 bf16 experts, 128 tokens: 144 against 159). For groups of 32 and
+// 64 four tiles' scales do not fit the registers. Four waves instead of
+// eight above 32 tokens: their sums fill the LDS. Outputs of up to 4096 rows
+// leave CUs idle unless each work-group has one tile (9 tokens over 64 fp4
+// experts, 2048 rows: 18.6 us against 23.6).
 template <class W, int TERMS>
 void launch_down(hipStream_t s, const DownArgs& d) {
     if constexpr (W::kWide) {
@@ -1165,7 +1174,7 @@ void launch_down(hipStream_t s, const DownArgs& d) {
             return d.T <= 32 ? launch_down<W, TERMS, 4, 8>(s, d) : launch_down<W, TERMS, 4, 4>(s, d);
     }
     if (d.T > 64) return launch_down<W, TERMS, 2, 4>(s, d);
-    if (tiles_of(d.w.N, 1) > DN_ONE) return launch_down<W, TERMS, 2, 8>(s, d);
+    if (tiles_of(d.w.N, 1) > 2 * kCus) return launch_down<W, TERMS, 2, 8>(s, d);
     launch_down<W, TERMS, 1, 8>(s, d);
 }
 

@@ -10,41 +10,50 @@ namespace {
 using namespace experts;
 
 constexpr int kPackThreads = 256;
+// Work-groups of a launch at most (a launch holds fewer than 2^32 threads,
+// and a model's experts have more groups of weights than that); each goes on
+// from its first piece in steps of the whole launch.
+constexpr unsigned kPackBlocks = 1u << 20;
 
 // One thread: the 32 codes that one lane of the product kernels loads at
 // once for one 8-row tile and 256 inputs: row lane % 8, and for each of the
 // block's four 64-input steps j the 8 inputs of vector lane_vec as one word.
-// In a word, int4 code m lies at bit 4 (m / 2) of half m % 2, so that a
-// shift and a mask leave two neighbours in the halves; 4-bit floats lie in
-// order, as the conversion instruction takes them. Rows past N and inputs
+// In a word, int4 code m lies at bit 4 (m / 2) + 3 of half m % 2 (the last
+// two run over into the next half, rotated), so that a shift or rotation and
+// a mask leave two neighbours at bits 3-6 of the halves, the upper mantissa
+// bits of a bf16; 4-bit floats lie in order, as the conversion instruction
+// takes them. Rows past N and inputs
 // past K get code 0.
 __global__ __launch_bounds__(kPackThreads) void pack_codes(const uint8_t* __restrict__ codes,
                                                            u32x4* __restrict__ out, int N, int K,
                                                            int tiles, int KB, int fp4,
                                                            size_t total) {
-    const size_t at = (size_t)blockIdx.x * kPackThreads + threadIdx.x;
-    if (at >= total) return;
-    const int lane = (int)(at & 63);
-    const size_t blk = at >> 6;
-    const int kb = (int)(blk % KB);
-    const size_t et = blk / KB;
-    const int row = (int)(et % tiles) * kTile + (lane & 7);
-    const size_t e = et / tiles;
-    u32x4 o = {0, 0, 0, 0};
-    if (row < N) {
-        const uint8_t* src = codes + (e * N + row) * (size_t)K;
+    for (size_t at = (size_t)blockIdx.x * kPackThreads + threadIdx.x; at < total;
+         at += (size_t)gridDim.x * kPackThreads) {
+        const int lane = (int)(at & 63);
+        const size_t blk = at >> 6;
+        const int kb = (int)(blk % KB);
+        const size_t et = blk / KB;
+        const int row = (int)(et % tiles) * kTile + (lane & 7);
+        const size_t e = et / tiles;
+        u32x4 o = {0, 0, 0, 0};
+        if (row < N) {
+            const uint8_t* src = codes + (e * N + row) * (size_t)K;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int k = kb * kPackK + j * kStep + lane_vec(lane) * 8;
-            uint32_t w = 0;
-            for (int m = 0; m < 8; ++m) {
-                const uint32_t q = k + m < K ? src[k + m] & 15u : 0u;
-                w |= q << (fp4 ? 4 * m : 4 * (m >> 1) + 16 * (m & 1));
+            for (int j = 0; j < 4; ++j) {
+                const int k = kb * kPackK + j * kStep + lane_vec(lane) * 8;
+                if (k >= K) continue;  // K is a multiple of 8
+                const u32x2 b = *(const u32x2*)(src + k);  // eight codes, one a byte
+                uint32_t w = 0;
+#pragma unroll
+                for (int m = 0; m < 8; ++m)
+                    w |= ((b[m >> 2] >> (8 * (m & 3))) & 15u)
+                         << (fp4 ? 4 * m : 4 * (m >> 1) + 16 * (m & 1));
+                o[j] = fp4 ? w : w << 3 | w >> 29;
             }
-            o[j] = w;
         }
+        out[at] = o;
     }
-    out[at] = o;
 }
 
 // [E,N,G] -> [E][tile][block][2 row quads][groups of the block][4 rows];
@@ -55,22 +64,23 @@ __global__ __launch_bounds__(kPackThreads) void pack_groups(const T* __restrict_
                                                             T* __restrict__ out, int N, int G,
                                                             int tiles, int KB, int per,
                                                             size_t total) {
-    const size_t at = (size_t)blockIdx.x * kPackThreads + threadIdx.x;
-    if (at >= total) return;
-    size_t r = at;
-    const int i = (int)(r & 3);
-    r >>= 2;
-    int gi = (int)(r % per);
-    r /= per;
-    const int quad = (int)(r & 1);
-    r >>= 1;
-    const int kb = (int)(r % KB);
-    r /= KB;
-    const int row = (int)(r % tiles) * kTile + quad * 4 + i;
-    const size_t e = r / tiles;
-    if (per == kPackK / 32) gi = (gi & 3) * 2 + (gi >> 2);
-    const int g = kb * per + gi;
-    out[at] = row < N && g < G ? src[(e * N + row) * (size_t)G + g] : (T)0;
+    for (size_t at = (size_t)blockIdx.x * kPackThreads + threadIdx.x; at < total;
+         at += (size_t)gridDim.x * kPackThreads) {
+        size_t r = at;
+        const int i = (int)(r & 3);
+        r >>= 2;
+        int gi = (int)(r % per);
+        r /= per;
+        const int quad = (int)(r & 1);
+        r >>= 1;
+        const int kb = (int)(r % KB);
+        r /= KB;
+        const int row = (int)(r % tiles) * kTile + quad * 4 + i;
+        const size_t e = r / tiles;
+        if (per == kPackK / 32) gi = (gi & 3) * 2 + (gi >> 2);
+        const int g = kb * per + gi;
+        out[at] = row < N && g < G ? src[(e * N + row) * (size_t)G + g] : (T)0;
+    }
 }
 
 // Symmetric quantization of one group per wave: s = amax / 7 (int4) or
@@ -81,48 +91,50 @@ __global__ __launch_bounds__(kPackThreads) void quant_groups(const uint16_t* __r
                                                              uint16_t* __restrict__ scales, int K,
                                                              int group, int G, int fp4, int f16,
                                                              size_t total) {
-    const size_t at = (size_t)blockIdx.x * (kPackThreads / kWave) + threadIdx.x / kWave;
-    if (at >= total) return;
     const int lane = lane_id();
-    const size_t row = at / G;
-    const int k0 = (int)(at % G) * group;
-    float v[2], amax = 0.0f;
+    constexpr int kPer = kPackThreads / kWave;
+    for (size_t at = (size_t)blockIdx.x * kPer + threadIdx.x / kWave; at < total;
+         at += (size_t)gridDim.x * kPer) {
+        const size_t row = at / G;
+        const int k0 = (int)(at % G) * group;
+        float v[2], amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int o = lane + i * kWave;
-        const bool in = o < group && k0 + o < K;
-        v[i] = in ? __uint_as_float((uint32_t)w[row * K + k0 + o] << 16) : 0.0f;
-        amax = fmaxf(amax, fabsf(v[i]));
-    }
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m, kWave));
-    const float s32 = amax / (fp4 ? 6.0f : 7.0f);
-    float s;
-    uint16_t bits;
-    if (f16) {
-        const _Float16 h = (_Float16)s32;
-        bits = __builtin_bit_cast(uint16_t, h);
-        s = (float)h;
-    } else {
-        bits = (uint16_t)bf16x2_bits(s32, 0.0f);
-        s = __uint_as_float((uint32_t)bits << 16);
-    }
-    if (lane == 0) scales[at] = bits;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int o = lane + i * kWave;
-        if (o >= group || k0 + o >= K) continue;
-        const float x = s > 0.0f ? v[i] / s : 0.0f;
-        uint32_t q;
-        if (fp4) {
-            const float a = fabsf(x);
-            q = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) +
-                (a >= 3.5f) + (a > 5.0f);
-            if (q && x < 0.0f) q |= 8u;
-        } else {
-            q = (uint32_t)((int)fminf(fmaxf(__builtin_rintf(x), -8.0f), 7.0f) + 8);
+        for (int i = 0; i < 2; ++i) {
+            const int o = lane + i * kWave;
+            const bool in = o < group && k0 + o < K;
+            v[i] = in ? __uint_as_float((uint32_t)w[row * K + k0 + o] << 16) : 0.0f;
+            amax = fmaxf(amax, fabsf(v[i]));
         }
-        codes[row * K + k0 + o] = (uint8_t)q;
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m, kWave));
+        const float s32 = amax / (fp4 ? 6.0f : 7.0f);
+        float s;
+        uint16_t bits;
+        if (f16) {
+            const _Float16 h = (_Float16)s32;
+            bits = __builtin_bit_cast(uint16_t, h);
+            s = (float)h;
+        } else {
+            bits = (uint16_t)bf16x2_bits(s32, 0.0f);
+            s = __uint_as_float((uint32_t)bits << 16);
+        }
+        if (lane == 0) scales[at] = bits;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int o = lane + i * kWave;
+            if (o >= group || k0 + o >= K) continue;
+            const float x = s > 0.0f ? v[i] / s : 0.0f;
+            uint32_t q;
+            if (fp4) {
+                const float a = fabsf(x);
+                q = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) +
+                    (a >= 3.5f) + (a > 5.0f);
+                if (q && x < 0.0f) q |= 8u;
+            } else {
+                q = (uint32_t)((int)fminf(fmaxf(__builtin_rintf(x), -8.0f), 7.0f) + 8);
+            }
+            codes[row * K + k0 + o] = (uint8_t)q;
+        }
     }
 }
 
@@ -137,7 +149,10 @@ size_t row_tiles(int N) { return ((size_t)N + kTile - 1) / kTile; }
 
 size_t blocks_of(int K) { return ((size_t)K + kPackK - 1) / kPackK; }
 
-dim3 blocks(size_t n, int per) { return dim3((unsigned)((n + per - 1) / per)); }
+dim3 blocks(size_t n, int per) {
+    const size_t b = (n + per - 1) / per;
+    return dim3(b < kPackBlocks ? (unsigned)b : kPackBlocks);
+}
 
 }  // namespace
 }  // namespace mep
@@ -164,7 +179,8 @@ extern "C" int mep_pack_weights(int E, int N, int K, int kind, int group, const 
         return MEP_ERR_PARAM;
     if (!codes || !scales || !packed_codes || !packed_scales) return MEP_ERR_NULLPTR;
     if (!rows::aligned16(packed_codes) || !rows::aligned16(packed_scales) ||
-        (packed_zeros && !rows::aligned16(packed_zeros)) || ((uintptr_t)scales & 1u))
+        (packed_zeros && !rows::aligned16(packed_zeros)) || ((uintptr_t)scales & 1u) ||
+        ((uintptr_t)codes & 7u))
         return MEP_ERR_SHAPE;
     hipStream_t s = (hipStream_t)stream;
     const int tiles = (int)row_tiles(N), KB = (int)blocks_of(K);

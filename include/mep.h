@@ -9,7 +9,11 @@
  *   - this rank's pack into per-destination send segments and the grouping
  *     of received rows by expert instance (mep_dispatch);
  *   - the score-weighted K-way reduction of returned expert outputs
- *     (mep_combine).
+ *     (mep_combine);
+ *   - for decode steps, the router's choice before all of these
+ *     (mep_route), the experts' products with 4-bit weights
+ *     (mep_expert_matvec) and the whole expert layer of a few tokens
+ *     (mep_moe_layer).
  *
  * Sources, cited by page title and section:
  *   [MoonEP-TD]  "MoonEP" technical overview (twodots.gr), architecture and
@@ -526,8 +530,9 @@ enum { MEP_SCORE_SOFTMAX = 0, MEP_SCORE_SIGMOID = 1 };
  *   scores[t,k] = scale * w[k] with w[k] = s[topk_ids[t,k]], 0 for -1;
  *          with renormalize, w is the softmax of the chosen logits, or
  *          s[k] / (sum of the chosen s + 1e-20).
- * c is formed and compared in fp64, so the choice does not hang on the
- * rounding of s. Note that mep_plan needs ids in [0, E): with fewer than K
+ * c is formed in fp64; groups are compared in it, experts on the upper 42
+ * bits of its mantissa (c that agree in them go to the lower id), so the
+ * choice does not hang on the rounding of s. Note that mep_plan needs ids in [0, E): with fewer than K
  * experts present use mep_moe_layer or a send map, which skip -1.
  *   logits [T,E] of logit_dtype (MEP_SCALE_*), bias [E] fp32 or NULL,
  *   topk_ids [T,K] int32, scores [T,K] fp32.
@@ -593,7 +598,8 @@ size_t mep_packed_scale_count(int E, int N, int K, int group);
 /*
  * mep_pack_weights - lays 4-bit weights out for mep_expert_matvec and
  * mep_moe_layer; once, when they are loaded.
- *   codes  [E,N,K] uint8, one code each in the low four bits;
+ *   codes  [E,N,K] uint8, one code each in the low four bits, 8-byte
+ *          aligned;
  *   scales [E,N,G] 16-bit floats, G = ceil(K / group), group i of a row
  *          covering inputs i*group and on;
  *   zeros  [E,N,G] uint8 (INT4: the value of code q is (q - zero) * scale;

@@ -114,8 +114,7 @@ def route_grad(l, ids, d, scoring, renormalize, scale):
 # ------------------------------------------------------------ 4-bit weights
 
 def decode(codes, scales, zeros, group, kind):
-    """[E,N,K] float64 values, and the largest magnitude any code offset can
-    have before it is taken out again (int4: 128 + q)."""
+    """[E,N,K] float64 values."""
     K = codes.shape[2]
     s = np.repeat(np.asarray(scales, np.float64), group, 2)[:, :, :K]
     if kind == "fp4":

@@ -83,6 +83,7 @@ def test_pack_and_quantize_validation(B):
     assert pack(a3=0) == pack(a3=3) == pack(a4=16) == B.MEP_ERR_PARAM
     assert pack(a7=P) == pack(a10=P) == pack(a3=2, a7=P, a10=P) == B.MEP_ERR_PARAM
     assert pack(a0=0) == pack(a2=20) == pack(a8=P + 8) == pack(a9=P + 8) == B.MEP_ERR_SHAPE
+    assert pack(a5=P + 4) == B.MEP_ERR_SHAPE
     q = [1, 16, 128, 1, 32, 1, P, P, P, None]
     for i in (6, 7, 8):
         assert B.mep_quant_weights(*q[:i], None, *q[i + 1:]) == B.MEP_ERR_NULLPTR

@@ -31,8 +31,8 @@ def _q4(rng, E, N, K, kind, group, zeros, scale="bf16", exact=False):
                     kind=kind)
     sv = st.double().numpy()
     val = ref.decode(codes, sv, z, group, kind)
-    # int4: |128 + q| + 136 (or 128 + z) per input
-    mag = np.abs(val) if kind == "fp4" else np.repeat(sv, group, 2)[:, :, :K] * 290.0
+    # int4: |16 + q| + 24 (or 16 + z) per input
+    mag = np.abs(val) if kind == "fp4" else np.repeat(sv, group, 2)[:, :, :K] * 56.0
     return w, val, mag
 
 
@@ -169,7 +169,7 @@ def test_quantize_pack_product_chain():
         torch.cuda.synchronize()
         sv = scales.double().cpu().numpy()[None]
         val = ref.decode(codes.cpu().numpy()[None], sv, None, 32, kind)[0]
-        mag = np.repeat(sv, 32, 2)[0, :, :520] * 290.0
+        mag = np.repeat(sv, 32, 2)[0, :, :520] * 56.0
         x64 = x.astype(np.float64)
         want = x64 @ val.T
         lim = ref.product_slack(np.abs(x64) @ mag.T, 520) + ref.U32 * np.abs(want)
@@ -491,7 +491,7 @@ def _q4_gpu(g, E, N, K, kind, group, zeros, dt, exact):
             v = table[codes[e].long()] * sv
             return v, v.abs()
         zv = 8.0 if z is None else z[e].double().repeat_interleave(group, 1)[:, :K]
-        return (codes[e].double() - zv) * sv, 290.0 * sv
+        return (codes[e].double() - zv) * sv, 56.0 * sv
     return w, dense
 
 
@@ -584,3 +584,27 @@ def test_layer_wide(kind, group, zeros, scale, T, K, E, H, I):
         half = ref.HALF["fp32" if f32 else "bf16"]
         err = (got.double() - want).abs()
         assert bool((err <= lim + half * (want.abs() + lim)).all()), float((err - lim).max())
+
+
+def test_quantize_and_pack_past_one_launch():
+    # more groups than one launch has waves for: the last rows are reached too
+    torch = require_gpu()
+    import combine_balancing_amd as cba
+    note("quantize large")
+    N, K, group = 40000, 4096, 32
+    g = torch.Generator(device="cuda").manual_seed(4)
+    w = torch.randn(N, K, generator=g, device="cuda").bfloat16()
+    codes, scales = cba.q4_quantize(w, group=group)
+    tail = w[-64:].float().view(64, K // group, group)
+    s = (tail.abs().amax(2) / 7).bfloat16()
+    assert torch.equal(scales[-64:], s)
+    want = torch.clamp(torch.round(tail / s.float()[..., None]), -8, 7) + 8
+    assert torch.equal(codes[-64:].view(64, K // group, group).float(), want)
+    q = cba.q4_pack(codes, scales, group=group)
+    x = torch.randint(-3, 4, (2, K), generator=g, device="cuda").bfloat16()
+    y = cba.expert_matvec_q4(x, q, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    val = (codes.double() - 8) * scales.double().repeat_interleave(group, 1)
+    ref64 = x.double() @ val.t()
+    lim = ref.product_slack(x.double().abs() @ (56.0 * scales.double().repeat_interleave(group, 1)).t(), K)
+    assert bool(((y.double() - ref64).abs() <= lim + ref.U32 * ref64.abs()).all())
