@@ -553,7 +553,7 @@ struct Finder {
     // routes: the slots, from work-group 0, and an expert's routes, from the
     // work-group that has its first rows.
     __device__ __forceinline__ void write_slots(Table* t) const {
-        if (blockIdx.x != 0 || blockIdx.y != 0 || threadIdx.x >= kWave) return;
+        if (blockIdx.x != 0 || blockIdx.y != 0 || blockIdx.z != 0 || threadIdx.x >= kWave) return;
         const int lane = lane_id();
         int s0 = 0, off = 0;
         for (int e0 = 0; e0 < kMaxExperts; e0 += kWave) {
@@ -759,10 +759,12 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void expert_rows_held(const RowsA
 // Products for more routes an expert: one work-group has RT tiles (LAYER: of
 // the gate rows, and the same of the up rows) of one slot, NW waves
 // splitting the inputs, and reads the inputs along with the weights, for up
-// to 16 routes at a time.
+// to 16 routes at a time; the passes of a crowded expert are shared among
+// gridDim.z work-groups.
 template <class W, bool LAYER, int RT, int NB, int NW>
 __device__ __forceinline__ void rows_pass(const RowsArgs& a, const Finder& find, f32x4* s_part,
-                                          int e, int cnt, int c0, int row0, Buffer xb) {
+                                          int e, int cnt, int c0, int row0, Buffer xb,
+                                          bool again) {
     constexpr int NT = LAYER ? 2 * RT : RT;
     const int lane = lane_id();
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x) / kWave;
@@ -781,7 +783,7 @@ __device__ __forceinline__ void rows_pass(const RowsArgs& a, const Finder& find,
         for (int i = 0; i < NT; ++i) acc[i][b] = f32x4{0, 0, 0, 0};
     }
     stream<W, 2, 1, NT, NB>(a.w, wp, xb, xp, KC * wave / NW, KC * (wave + 1) / NW, lane, acc);
-    if (c0) lds_barrier();  // the last pass's sums have been read
+    if (again) lds_barrier();  // the last pass's sums have been read
     // [wave][tile][block][32]
     if ((i16 < 8) == (q < 2)) {
 #pragma unroll
@@ -847,18 +849,16 @@ __global__ __launch_bounds__(NW* kWave, 2) void expert_rows_read(const RowsArgs 
         int off;
         cnt = s_find.find(a, few, e, &off);
         if constexpr (LAYER) {
-            if (blockIdx.x == 0) s_find.write_routes(a, off, cnt);
+            if (blockIdx.x == 0 && blockIdx.z == 0) s_find.write_routes(a, off, cnt);
         }
     }
     const Buffer xb = buffer_of(a.x, (uint32_t)(a.n / a.div) * a.w.KV * 16u);
-    for (int c0 = 0; c0 < cnt;) {
-        if (cnt - c0 > kCols) {
-            rows_pass<W, LAYER, RT, 2, NW>(a, s_find, s_part, e, cnt, c0, row0, xb);
-            c0 += 2 * kCols;
-        } else {
-            rows_pass<W, LAYER, RT, 1, NW>(a, s_find, s_part, e, cnt, c0, row0, xb);
-            c0 += kCols;
-        }
+    const int c1 = blockIdx.z * 2 * kCols, step = gridDim.z * 2 * kCols;
+    for (int c0 = c1; c0 < cnt; c0 += step) {
+        if (cnt - c0 > kCols)
+            rows_pass<W, LAYER, RT, 2, NW>(a, s_find, s_part, e, cnt, c0, row0, xb, c0 > c1);
+        else
+            rows_pass<W, LAYER, RT, 1, NW>(a, s_find, s_part, e, cnt, c0, row0, xb, c0 > c1);
     }
 }
 
@@ -924,22 +924,22 @@ __global__ __launch_bounds__(NW* kWave, 2) void expert_down(const DownArgs a) {
                 (uint32_t)(at + j * 2 * kRoutes)};
         if (lane == kWave - 1) s_jobs = to;
     } else {
-        const int n_slots = a.table->n_slots;
-        const int live = n_slots ? a.table->offset[n_slots] : 0;
-        for (int i = tid; i < live; i += NW * kWave) {
-            const int r = a.table->route[i];
+        // Loads that do not wait for each other: entries past the last slot
+        // or route are read (they lie in the table) and not used.
+        const int n_slots = a.table->n_slots, slots_max = min(a.n, a.E);
+        for (int i = tid; i < a.n; i += NW * kWave) {
+            const int r = min((int)a.table->route[i], a.n - 1);
             s_route[i] = (uint16_t)r;
             s_score[i] = a.scores[r];
             s_token[i] = (uint8_t)(r / a.K);
         }
         if (wave == 0) {
             int jobs = 0;
-            for (int s0 = 0; s0 < n_slots; s0 += kWave) {
-                const int s = s0 + lane;
-                const bool in = s < n_slots;
-                const int e = in ? a.table->expert[s] : 0;
-                const int off = in ? a.table->offset[s] : 0;
-                const int cnt = in ? a.table->offset[s + 1] - off : 0;
+            for (int s0 = 0; s0 < slots_max; s0 += kWave) {
+                const int s = min(s0 + lane, slots_max - 1);
+                const int e = a.table->expert[s], off = a.table->offset[s];
+                const int to_off = a.table->offset[s + 1];
+                const int cnt = s0 + lane < n_slots ? to_off - off : 0;
                 const int mine = (cnt + 2 * kRoutes - 1) / (2 * kRoutes);
                 const int to = jobs + wave_inclusive_sum(mine);
                 for (int j = 0; j < mine; ++j)
@@ -1145,7 +1145,14 @@ void launch_rows(hipStream_t s, const RowsArgs& a) {
         return;
     }
     constexpr int RT = 2, NW = 4;
-    hipLaunchKernelGGL((expert_rows_read<W, LAYER, RT, NW>), dim3(tiles_of(rows, RT), slots),
+    // Few work-groups: the passes over 16 routes that an expert has on average
+    // run beside each other (86 rows of one 600x3144 matrix: 8 us against
+    // 21 one after the other). With many, one work-group goes through them
+    // and finds the weights in its caches.
+    const int tiles = tiles_of(rows, RT), passes = (a.n / slots + 2 * kCols - 1) / (2 * kCols);
+    const int room = 4 * kCus / (tiles * slots);
+    const int z = passes < room ? passes : room;
+    hipLaunchKernelGGL((expert_rows_read<W, LAYER, RT, NW>), dim3(tiles, slots, z < 1 ? 1 : z),
                        dim3(NW * kWave), 0, s, a);
 }
 
@@ -1164,17 +1171,17 @@ void launch_down(hipStream_t s, const DownArgs& d) {
 // moves (64 int4 experts, 32 tokens: 142 us against 176 with two tiles; a
 // rank's 32 bf16 experts, 128 tokens: 144 against 159). For groups of 32 and
 // 64 four tiles' scales do not fit the registers. Four waves instead of
-// eight above 32 tokens: their sums fill the LDS. Outputs of up to 4096 rows
+// eight above 32 tokens: their sums fill the LDS. Outputs of up to 5120 rows
 // leave CUs idle unless each work-group has one tile (9 tokens over 64 fp4
-// experts, 2048 rows: 18.6 us against 23.6).
+// experts, 2048 rows: 18.6 us against 23.6; 89 tokens, 232 rows, both
+// kernels: 23 us against 29).
 template <class W, int TERMS>
 void launch_down(hipStream_t s, const DownArgs& d) {
     if constexpr (W::kWide) {
         if (tiles_of(d.w.N, 4) >= kCus * 3 / 4)
             return d.T <= 32 ? launch_down<W, TERMS, 4, 8>(s, d) : launch_down<W, TERMS, 4, 4>(s, d);
     }
-    if (d.T > 64) return launch_down<W, TERMS, 2, 4>(s, d);
-    if (tiles_of(d.w.N, 1) > 2 * kCus) return launch_down<W, TERMS, 2, 8>(s, d);
+    if (tiles_of(d.w.N, 1) > kCus * 5 / 2) return launch_down<W, TERMS, 2, 4>(s, d);
     launch_down<W, TERMS, 1, 8>(s, d);
 }
 

@@ -537,6 +537,8 @@ void dispatch_route(hipStream_t s, bool sig, const void* logits, const float* bi
         MEP_TRY(16, 4)
         MEP_TRY(16, 8)
         MEP_TRY(16, 16)
+        MEP_TRY(32, 4)
+        MEP_TRY(32, 8)
         MEP_TRY(32, 12)
         MEP_TRY(32, 16)
     }

@@ -246,6 +246,50 @@ def test_layer_sizes(kind, group, T, K, E, H, I):
     _layer_check(np.random.default_rng(T + H), T, K, E, H, I, kind, group)
 
 
+@pytest.mark.parametrize("kind,group", [("bf16", 0), ("int4", 128), ("fp4", 64)])
+@pytest.mark.parametrize("T,K", [(16, 4), (13, 5), (128, 16), (1, 64), (1, 65), (32, 2)])
+def test_layer_most_experts(kind, group, T, K):
+    # 1024 experts, the last among them; 64 routes and one more
+    require_gpu()
+    note(f"layer 1024 experts {kind} {(T, K)}")
+    rng = np.random.default_rng(T * K)
+    ids = rng.integers(0, 1024, (T, K)).astype(np.int32)
+    ids[0, 0], ids[-1, -1] = 1023, 0
+    _layer_check(rng, T, K, 1024, 16, 8, kind, group, ids=ids, first=0)
+
+
+def test_products_graph():
+    torch = require_gpu()
+    import combine_balancing_amd as cba
+    note("products graph")
+    rng = np.random.default_rng(77)
+    w, _, _ = _q4(rng, 6, 70, 264, "int4", 64, True)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    for T, R in ((5, 4), (40, 3)):
+        x = torch.randn(T, 264, device="cuda", generator=g).bfloat16()
+        ids = torch.randint(-1, 6, (T, R), device="cuda", generator=g, dtype=torch.int32)
+        out = torch.zeros(T, R, 70, device="cuda")
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            cba.expert_matvec_q4(x, w, ids=ids, out=out)
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            cba.expert_matvec_q4(x, w, ids=ids, out=out)
+        for _ in range(3):
+            x.copy_(torch.randn(T, 264, device="cuda", generator=g))
+            ids.copy_(torch.randint(-1, 6, (T, R), device="cuda", generator=g, dtype=torch.int32))
+            out.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            got = out.clone()
+            out.zero_()
+            cba.expert_matvec_q4(x, w, ids=ids, out=out)
+            torch.cuda.synchronize()
+            assert torch.equal(got, out)
+
+
 @pytest.mark.parametrize("kind,group", [("bf16", 0), ("int4", 64), ("fp4", 128)])
 def test_layer_masks_repeats_and_empty(kind, group):
     require_gpu()
