@@ -84,8 +84,8 @@ __global__ __launch_bounds__(kPackThreads) void pack_groups(const T* __restrict_
 }
 
 // Symmetric quantization of one group per wave: s = amax / 7 (int4) or
-// amax / 6 (4-bit float) rounded to the scale's type, codes the nearest of
-// fl(w / s), ties to even.
+// amax / 6 (4-bit float) rounded to the scale's type, at most its largest
+// finite value; codes the nearest of fl(w / s), ties to even.
 __global__ __launch_bounds__(kPackThreads) void quant_groups(const uint16_t* __restrict__ w,
                                                              uint8_t* __restrict__ codes,
                                                              uint16_t* __restrict__ scales, int K,
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(kPackThreads) void quant_groups(const uint16_t* __r
         float s;
         uint16_t bits;
         if (f16) {
-            const _Float16 h = (_Float16)s32;
+            const _Float16 h = (_Float16)fminf(s32, 65504.0f);  // codes then stop at their ends
             bits = __builtin_bit_cast(uint16_t, h);
             s = (float)h;
         } else {

@@ -28,6 +28,7 @@ constexpr int kRouteMaxE = 1024;
 constexpr int kRouteMaxK = 64;  // one lane per chosen expert
 constexpr int kRouteMaxGroups = 64;
 constexpr int kRouteManyTokens = 4096;
+constexpr int kRouteMaxT = 1 << 26;  // a launch holds fewer than 2^32 threads, up to 64 a token
 constexpr double kRenormEps = 1e-20;  // sigmoid scores may all round to zero
 
 template <typename T>
@@ -473,7 +474,6 @@ __global__ __launch_bounds__(kRouteThreads) void route_grad_lanes(
         const double r = z > 0.0 ? 1.0 / z : 0.0;
         const double s = live ? exp_neg((double)lj - top) * r : 0.0;
         const double dot = lanes_sum<L>(g * s);
-        dl = s * (g - dot);
         double twice = 0.0;  // an id given again adds its g
         for (int k = 0; k < K; ++k) {
             const double o = __shfl(g, base + k, kWave);
@@ -623,8 +623,8 @@ extern "C" int mep_route(int T, int E, int K, const void* logits, int logit_dtyp
                          const float* bias, int scoring, int n_group, int topk_group,
                          int renormalize, float scale, int32_t* topk_ids, float* scores,
                          void* stream) {
-    if (T < 0 || E < 1 || E > kRouteMaxE || K < 1 || K > kRouteMaxK ||
-        (long long)T * E >= (1ll << 40) || (long long)T * K >= (1ll << 31))
+    if (T < 0 || T >= kRouteMaxT || E < 1 || E > kRouteMaxE || K < 1 || K > kRouteMaxK ||
+        (long long)T * K >= (1ll << 31))
         return MEP_ERR_SHAPE;
     if (n_group < 1 || n_group > kRouteMaxGroups || E % n_group != 0 || topk_group < 1 ||
         topk_group > n_group || K > topk_group * (E / n_group) || !known_dtype(logit_dtype) ||
@@ -650,8 +650,8 @@ extern "C" int mep_route(int T, int E, int K, const void* logits, int logit_dtyp
 extern "C" int mep_route_grad(int T, int E, int K, const void* logits, int logit_dtype,
                               const int32_t* topk_ids, const float* dscores, int scoring,
                               int renormalize, float scale, void* dlogits, void* stream) {
-    if (T < 0 || E < 1 || E > kRouteMaxE || K < 1 || K > kRouteMaxK || K > E ||
-        (long long)T * E >= (1ll << 40) || (long long)T * K >= (1ll << 31))
+    if (T < 0 || T >= kRouteMaxT || E < 1 || E > kRouteMaxE || K < 1 || K > kRouteMaxK || K > E ||
+        (long long)T * K >= (1ll << 31))
         return MEP_ERR_SHAPE;
     if (!known_dtype(logit_dtype) ||
         (scoring != MEP_SCORE_SOFTMAX && scoring != MEP_SCORE_SIGMOID) ||

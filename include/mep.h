@@ -530,14 +530,15 @@ enum { MEP_SCORE_SOFTMAX = 0, MEP_SCORE_SIGMOID = 1 };
  *   scores[t,k] = scale * w[k] with w[k] = s[topk_ids[t,k]], 0 for -1;
  *          with renormalize, w is the softmax of the chosen logits, or
  *          s[k] / (sum of the chosen s + 1e-20).
- * c is formed in fp64; groups are compared in it, experts on the upper 42
- * bits of its mantissa (c that agree in them go to the lower id), so the
- * choice does not hang on the rounding of s. Note that mep_plan needs ids in [0, E): with fewer than K
- * experts present use mep_moe_layer or a send map, which skip -1.
+ * c is formed in fp64; groups are compared in it, experts on at least the
+ * upper 42 bits of its mantissa (c that agree in what is compared go to the
+ * lower id), so the choice does not hang on the rounding of s. Note that
+ * mep_plan needs ids in [0, E): with fewer than K experts present use
+ * mep_moe_layer or a send map, which skip -1.
  *   logits [T,E] of logit_dtype (MEP_SCALE_*), bias [E] fp32 or NULL,
  *   topk_ids [T,K] int32, scores [T,K] fp32.
- * Sizes: T >= 0 (0 does nothing), 1 <= E <= 1024, 1 <= K <= 64,
- * T*K < 2^31, T*E < 2^40.
+ * Sizes: 0 <= T < 2^26 (0 does nothing), 1 <= E <= 1024, 1 <= K <= 64,
+ * T*K < 2^31.
  * Errors: MEP_ERR_NULLPTR, MEP_ERR_PARAM (n_group not in [1, 64] or no
  * divisor of E, topk_group not in [1, n_group], K above the experts that the
  * kept groups hold, unknown dtype or scoring, scale not finite),
@@ -615,7 +616,8 @@ int mep_pack_weights(int E, int N, int K, int kind, int group, const uint8_t* co
  * mep_quant_weights - codes and scales (as mep_pack_weights takes them) of
  * bf16 matrices, symmetric, per row and group:
  *   scale = fl(max |w| / 7) (INT4) or fl(max |w| / 6) (FP4) rounded to
- *           scale_dtype (MEP_SCALE_BF16 or MEP_SCALE_F16)
+ *           scale_dtype (MEP_SCALE_BF16 or MEP_SCALE_F16), at most 65504 in
+ *           the latter
  *   code  = the nearest to fl(w / scale), ties to even; INT4 clamped to
  *           [-8, 7] and stored plus 8; FP4 clamped to +-6; zero where
  *           scale == 0
@@ -657,7 +659,8 @@ size_t mep_moe_layer_workspace_size(int T, int K, int I);
  * weight tensor as mep_plan_weight_rows names them) and its mask byte (its
  * balanced_mask) is not 0; a token without one gets a zero row. Sums are
  * fp32; between the two kernels h keeps 24 bits of mantissa when out_f32 is
- * given and 16 when not; the output is rounded once. Every sum has a fixed order.
+ * given and 16 when not; the output is rounded once. Every sum has a fixed
+ * order.
  *   x [T,H] bf16; ids [T*K] int32; scores [T*K] fp32; mask [T*K] uint8 or
  *   NULL; w13 [E, 2I, H] and w2 [E, H, I] of one kind, group and scale type;
  *   out_bf16, out_f32 [T,H], either may be NULL but not both; workspace of

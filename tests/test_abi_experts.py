@@ -56,6 +56,13 @@ def test_route_grad_validation(B):
     assert _grad(B, T=0, logits=None, ids=None, d=None, dl=None) == B.MEP_OK
 
 
+def test_route_tokens_of_one_launch(B):
+    # up to 64 threads a token, fewer than 2^32 a launch
+    for T in (2 ** 26, 2 ** 31 - 1):
+        assert _route(B, T=T, E=1, K=1) == B.MEP_ERR_SHAPE
+        assert _grad(B, T=T, E=1, K=1) == B.MEP_ERR_SHAPE
+
+
 def _w(B, kind=1, E=2, N=16, K=128, group=32, sd=1, data=P, scales=P, zeros=None):
     return B.Weights(kind, E, N, K, group, sd, data, scales, zeros)
 

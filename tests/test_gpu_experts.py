@@ -153,6 +153,27 @@ def test_quantize(kind, scale, E, N, K, group):
             assert np.array_equal(c, want)
 
 
+@pytest.mark.parametrize("kind", ["int4", "fp4"])
+def test_quantize_past_fp16_scales(kind):
+    # max |w| / 7 above fp16's range: the scale is its largest finite value
+    # and the codes stop at their ends
+    torch = require_gpu()
+    import combine_balancing_amd as cba
+    note(f"quantize past fp16 {kind}")
+    w = torch.zeros(2, 64, dtype=torch.bfloat16)
+    w[0, 3], w[0, 4], w[0, 40], w[1, 0] = 2.0 ** 20, -(2.0 ** 30), 65536.0, 3e38
+    codes, scales = cba.q4_quantize(w.cuda(), group=32, kind=kind, scale_dtype=torch.float16)
+    torch.cuda.synchronize()
+    codes, scales = codes.cpu(), scales.cpu()
+    low = torch.tensor(65536.0 / (6 if kind == "fp4" else 7)).half()
+    assert scales[0].tolist() == [65504.0, low.item()] and scales[1].tolist() == [65504.0, 0.0]
+    # 2^20 / 65504 is past either kind's largest value, as is -2^30 / 65504
+    # (int4's lowest is -8)
+    ends = [7, 15, 7] if kind == "fp4" else [15, 0, 15]
+    assert [int(codes[0, 3]), int(codes[0, 4]), int(codes[1, 0])] == ends
+    assert int(codes[0, 40]) == (7 if kind == "fp4" else 15)
+
+
 def test_quantize_pack_product_chain():
     # weights through q4_quantize, q4_pack and the product: the result is the
     # product with the quantized values, and near the one with the originals
