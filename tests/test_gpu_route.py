@@ -95,6 +95,23 @@ def test_route_many_tokens(dtype, E, ng, tg, K):
         assert np.all(np.abs(got - want) <= SCORE_TOL * np.abs(want) + 2.0 ** -149)
 
 
+@pytest.mark.parametrize("T", [3, 4096])
+@pytest.mark.parametrize("E,K", [(64, 4), (64, 5), (128, 9), (256, 8), (256, 9), (256, 16),
+                                 (384, 8), (384, 13), (1024, 8), (1024, 17), (1024, 64)])
+def test_route_chosen_side_by_side(T, E, K):
+    # logits in order: one lane's experts are chosen to the last, then the next's
+    torch = require_gpu()
+    import combine_balancing_amd as cba
+    note(f"route side by side T={T} E={E} K={K}")
+    up = torch.arange(E, dtype=torch.float32) / 64 - E / 128
+    l = torch.stack([up, up.flip(0), up.roll(E // 2 + 3)])
+    full = l.repeat(-(-T // 3), 1)[:T].contiguous().cuda()
+    ids, _ = cba.route(full, K)
+    torch.cuda.synchronize()
+    want = torch.argsort(l.double(), 1, descending=True)[:, :K].int()
+    assert torch.equal(ids.cpu(), want.repeat(-(-T // 3), 1)[:T])
+
+
 @pytest.mark.parametrize("offset", [1, 2, 4])
 def test_route_off_the_vector_grid(offset):
     # logits that start inside a larger buffer, `offset` elements in
